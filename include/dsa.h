@@ -442,6 +442,134 @@ int dsa_sparse_mla_decode_paged(const void *q, const void *kv_pool,
                                 dsa_stream_t stream);
 
 /*
+ * Attention of the new tokens over the whole paged latent cache, split over
+ * its length: the results of dsa_dense_causal_mla_decode_paged (the dense
+ * interface page 2 keeps beside DSA, "六、实测表现与取舍"), for few or long
+ * sequences too. The keys of all sequences are cut into equal shares of work,
+ * whatever sequence they belong to, so one sequence of 131072 tokens uses the
+ * whole GPU; the partial softmaxes of a sequence are joined by a second
+ * launch. The pages describe no split; the method is the usual one of
+ * combining partial sums by their maxima.
+ *
+ *   q            [B][nq][H][576] bf16, 16-byte aligned
+ *   kv_pool      [nblk][64][576] bf16, block_table [B][max_blocks]
+ *   seq_len      [B] int32, 0 .. 64 * max_blocks: query j of sequence b sits
+ *                at position seq_len[b] - nq + j and sees the keys up to its
+ *                own. A query at a negative position (a padded sequence of
+ *                no or few tokens) sees none: out 0, lse -inf. A length out
+ *                of range is clamped and recorded as DSA_ERR_DEVICE_BOUNDS.
+ *   out, lse     as for dsa_dense_causal_mla_decode_paged; lse may be NULL
+ *   workspace    dsa_split_mla_decode_workspace_size(B, nq, max_blocks, H)
+ *                bytes, 256-byte aligned; nothing in it is kept between
+ *                calls. Calls that may run at the same time (and captured
+ *                graphs that may replay at the same time) need one each.
+ * Keys past seq_len and table entries past its last block are not read as
+ * keys: whatever they hold, NaN included, has no effect. A block id outside
+ * [0, nblk) is recorded as DSA_ERR_DEVICE_BOUNDS and its 64 keys are skipped.
+ * Returns DSA_ERR_UNSUPPORTED for H outside 1 .. 128, DSA_ERR_WORKSPACE for a
+ * missing, misaligned or short workspace.
+ */
+size_t dsa_split_mla_decode_workspace_size(int B, int nq, int max_blocks, int H);
+int dsa_split_mla_decode_paged(const void *q, const void *kv_pool, const int32_t *block_table,
+                               const int32_t *seq_len, int B, int nq, int max_blocks, int nblk,
+                               int H, float sm_scale, void *out, float *lse, void *workspace,
+                               size_t ws_bytes, dsa_stream_t stream);
+
+/*
+ * Sliding-window attention (page 1, section "秘密武器"; page 4, section
+ * "Sparse Attention") whose first few tokens stay visible: a query at
+ * position p sees the keys s <= p with s > p - window or s < sinks. Only the
+ * cache blocks a query sees are read, and no index sets are made (compare
+ * dsa_window_indices). The pages name the window and no sinks: keeping the
+ * first tokens visible is this library's addition for models whose attention
+ * rests on them; sinks = 0 is the pages' window.
+ *
+ * dsa_window_mla: rows t = 0 .. T-1 at positions q_pos0 + t over the
+ *   contiguous cache kv [S][576]; keys past S - 1 do not exist, so a row far
+ *   past the cache may see no key (out 0, lse -inf). q_pos0 + T and S at most
+ *   2^30. window >= q_pos0 + T is dense causal attention.
+ *   workspace: dsa_window_mla_workspace_size(T, S, H, q_pos0, sinks, window)
+ *   bytes (few rows are split over the keys, as in a decode; 0 for many).
+ * dsa_window_mla_decode_paged: the same mask for the nq new tokens of each
+ *   sequence of a paged cache; arguments, workspace and faults as for
+ *   dsa_split_mla_decode_paged. Blocks no query sees may have any table entry.
+ * sinks >= 0, window >= 1.
+ */
+size_t dsa_window_mla_workspace_size(int T, int S, int H, int q_pos0, int sinks, int window);
+int dsa_window_mla(const void *q, const void *kv, int T, int S, int H, int q_pos0, int sinks,
+                   int window, float sm_scale, void *out, float *lse, void *workspace,
+                   size_t ws_bytes, dsa_stream_t stream);
+int dsa_window_mla_decode_paged(const void *q, const void *kv_pool, const int32_t *block_table,
+                                const int32_t *seq_len, int B, int nq, int max_blocks, int nblk,
+                                int H, int sinks, int window, float sm_scale, void *out,
+                                float *lse, void *workspace, size_t ws_bytes,
+                                dsa_stream_t stream);
+
+/*
+ * The attention weight each cached token receives from the new tokens, added
+ * to its running total (what dsa_cache_evict_paged ranks tokens by). The
+ * pages' warm-up (page 2, "四、训练的两步走冷启动") records the same
+ * distribution for training, see dsa_attention_probs_mean; this is its sum
+ * over heads and queries for a paged cache, without logits in memory.
+ *
+ *   w[b][s] = sum over j, h with s <= seq_len[b] - nq + j of
+ *             exp(sm_scale q[b,j,h] . kv[s] - lse[b,j,h])
+ *   mass[b][s] = (s < seq_len[b] - nq ? mass[b][s] : 0) + w[b][s],
+ *             s < seq_len[b]: a new token's total starts here, so its slot
+ *             needs no clearing; entries from seq_len[b] on are not written
+ *
+ *   lse     [B][nq][H] fp32 as dsa_split_mla_decode_paged returns it for the
+ *           same queries; a query whose lse is -inf gives nothing
+ *   mass    [B][ld] fp32, indexed by the token's slot, ld >= 64 * max_blocks
+ *   other arguments and faults as for dsa_split_mla_decode_paged; the keys of
+ *   a bad block id keep their totals. Every total is summed by one thread in
+ *   one order: the same inputs give the same bits.
+ */
+int dsa_attention_mass_paged(const void *q, const void *kv_pool, const int32_t *block_table,
+                             const int32_t *seq_len, const float *lse, int B, int nq,
+                             int max_blocks, int nblk, int H, float sm_scale, float *mass,
+                             int64_t ld, dsa_stream_t stream);
+
+/*
+ * Eviction from the paged caches by accumulated attention weight, in place.
+ * The pages keep every token; this is the companion of the dense and windowed
+ * decode above for contexts that outgrow the cache.
+ *
+ * A sequence of at most `budget` tokens is left as it is. A longer one keeps
+ * its first `sinks` tokens, its last `recent` tokens and, of those between,
+ * the budget - sinks - recent of the largest totals (ties to the smaller
+ * slot; a NaN total ranks below every other). The kept tokens move to the
+ * sequence's slots 0 .. budget - 1 in their order, in every pool given, so
+ * that the blocks past the new length are free for the caller to reuse. A
+ * slot is a token's place in the cache, no longer its position in the text
+ * (rotary phases are part of the cached rows and move with them).
+ *
+ *   kv_pool       [nblk][64][576] bf16, 16-byte aligned
+ *   k8_pool       [nblk][64][128] e4m3, 16-byte aligned, or NULL
+ *   k_scale_pool  [nblk][64] fp32, or NULL
+ *   block_table   [B][max_blocks]; the blocks of a sequence that is evicted
+ *                 from must belong to it alone
+ *   seq_len       [B] int32 (clamped to 0 .. 64 * max_blocks, as above)
+ *   mass          [B][ld] fp32 totals by slot, ld >= 64 * max_blocks
+ *   budget        >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget
+ *   idx           [B][budget] int32 out: the slots kept, ascending, -1 past
+ *                 the new length (slot j of the new cache held slot idx[j])
+ *   seq_len_out   [B] int32 out: min(seq_len, budget); may be seq_len itself
+ *   mass_out      [B][ld_out] out: the kept totals in their new slots, or
+ *                 NULL; may be mass itself (ld_out = ld), else may not
+ *                 overlap it; ld_out >= min(budget, 64 * max_blocks); entries
+ *                 past the new length are not written
+ * Rows past the new length keep their bytes. A block id outside [0, nblk) is
+ * recorded as DSA_ERR_DEVICE_BOUNDS and the rows it holds do not move.
+ * B at most 65535 (DSA_ERR_UNSUPPORTED).
+ */
+int dsa_cache_evict_paged(void *kv_pool, void *k8_pool, float *k_scale_pool,
+                          const int32_t *block_table, const int32_t *seq_len, const float *mass,
+                          int64_t ld, int B, int max_blocks, int nblk, int budget, int sinks,
+                          int recent, int32_t *idx, int32_t *seq_len_out, float *mass_out,
+                          int64_t ld_out, dsa_stream_t stream);
+
+/*
  * Splitting the work over several GPUs (host only: no CUDA call, nothing
  * launched). The pages describe no distributed step; every prefill row and
  * every decode sequence is independent given the caches, which each GPU

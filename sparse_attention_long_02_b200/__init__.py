@@ -67,6 +67,15 @@ _sig("dsa_plan_prefill_chunks", I32, I32, I32, I32, I32, I32, I32, I32, I32, I32
 _sig("dsa_plan_decode_sequences", I32, P, I32, I32, I32, I32, I32, I32, I32, P, I32)
 _sig("dsa_dense_causal_mla", I32, P, P, I32, I32, I32, I32, F32, P, P, P)
 _sig("dsa_dense_causal_mla_decode_paged", I32, P, P, P, P, I32, I32, I32, I32, I32, F32, P, P, P)
+_sig("dsa_split_mla_decode_workspace_size", SZ, I32, I32, I32, I32)
+_sig("dsa_split_mla_decode_paged", I32, P, P, P, P, I32, I32, I32, I32, I32, F32, P, P, P, SZ, P)
+_sig("dsa_window_mla_workspace_size", SZ, I32, I32, I32, I32, I32, I32)
+_sig("dsa_window_mla", I32, P, P, I32, I32, I32, I32, I32, I32, F32, P, P, P, SZ, P)
+_sig("dsa_window_mla_decode_paged", I32, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, F32, P, P,
+     P, SZ, P)
+_sig("dsa_attention_mass_paged", I32, P, P, P, P, P, I32, I32, I32, I32, I32, F32, P, I64, P)
+_sig("dsa_cache_evict_paged", I32, P, P, P, P, P, P, I64, I32, I32, I32, I32, I32, I32, P, P, P,
+     I64, P)
 _sig("dsa_sparse_mla_decode_paged", I32, P, P, P, P, P, I32, I32, I32, I32, I32, I32, F32, P,
      P, P)
 
@@ -435,6 +444,140 @@ def dense_causal_mla_decode_paged(q, kv_pool, block_table, seq_len, sm_scale, ou
                                                   _p(lse), _stream(stream)),
            "dsa_dense_causal_mla_decode_paged")
     return out, lse
+
+
+def _shaped(t, dtype, *shape):
+    """`t` on the current device, contiguous, of that type and shape (-1: any extent)."""
+    t = _dev(t, dtype)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensor is on {t.device}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    if t.dim() != len(shape) or any(e not in (-1, n) for n, e in zip(t.shape, shape)):
+        raise ValueError(f"expected shape {list(shape)} (-1: any), got {list(t.shape)}")
+    return t
+
+
+def _paged_cache(kv_pool, block_table, seq_len):
+    _shaped(kv_pool, torch.bfloat16, -1, 64, 576)
+    _shaped(block_table, torch.int32, -1, -1)
+    _shaped(seq_len, torch.int32, block_table.shape[0])
+
+
+def split_mla_decode_workspace_size(B, nq, max_blocks, H) -> int:
+    return int(_lib.dsa_split_mla_decode_workspace_size(B, nq, max_blocks, H))
+
+
+def _range_decode(fn, q, kv_pool, block_table, seq_len, extra, sm_scale, out, lse, workspace,
+                  stream):
+    _paged_cache(kv_pool, block_table, seq_len)
+    B, max_blocks = block_table.shape
+    _shaped(q, torch.bfloat16, B, -1, -1, 576)
+    nq, H = q.shape[1], q.shape[2]
+    dev = q.device
+    if out is None:
+        out = torch.empty(B, nq, H, 512, dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty(B, nq, H, dtype=torch.float32, device=dev)
+    _shaped(out, torch.bfloat16, B, nq, H, 512)
+    _shaped(lse, torch.float32, B, nq, H)
+    if workspace is None:
+        need = split_mla_decode_workspace_size(B, nq, max_blocks, H)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+    _check(getattr(_lib, fn)(_p(q), _p(kv_pool), _p(block_table), _p(seq_len), B, nq, max_blocks,
+                             kv_pool.shape[0], H, *extra, float(sm_scale), _p(out), _p(lse),
+                             _p(_dev(workspace)), workspace.numel() * workspace.element_size(),
+                             _stream(stream)), fn)
+    return out, lse
+
+
+def split_mla_decode_paged(q, kv_pool, block_table, seq_len, sm_scale, out=None, lse=None,
+                           workspace=None, stream=None):
+    """Dense attention of the new tokens over the whole paged latent cache, split
+    over its length -> (out [B][nq][H][512], lse [B][nq][H])."""
+    return _range_decode("dsa_split_mla_decode_paged", q, kv_pool, block_table, seq_len, (),
+                         sm_scale, out, lse, workspace, stream)
+
+
+def window_mla_decode_paged(q, kv_pool, block_table, seq_len, sinks, window, sm_scale, out=None,
+                            lse=None, workspace=None, stream=None):
+    """Attention of the new tokens over a sliding window of the paged latent cache
+    and its first `sinks` tokens -> (out, lse); workspace as split_mla_decode_paged."""
+    return _range_decode("dsa_window_mla_decode_paged", q, kv_pool, block_table, seq_len,
+                         (sinks, window), sm_scale, out, lse, workspace, stream)
+
+
+def window_mla_workspace_size(T, S, H, q_pos0, sinks, window) -> int:
+    return int(_lib.dsa_window_mla_workspace_size(T, S, H, q_pos0, sinks, window))
+
+
+def window_mla(q, kv, sinks, window, sm_scale, q_pos0=0, out=None, lse=None, workspace=None,
+               stream=None):
+    """Prefill whose row t sees a window of keys ending at q_pos0 + t and the first
+    `sinks` keys -> (out [T][H][512], lse [T][H])."""
+    _shaped(q, torch.bfloat16, -1, -1, 576)
+    _shaped(kv, torch.bfloat16, -1, 576)
+    T, H, S = q.shape[0], q.shape[1], kv.shape[0]
+    if out is None:
+        out = torch.empty(T, H, 512, dtype=torch.bfloat16, device=q.device)
+    if lse is None:
+        lse = torch.empty(T, H, dtype=torch.float32, device=q.device)
+    _shaped(out, torch.bfloat16, T, H, 512)
+    _shaped(lse, torch.float32, T, H)
+    if workspace is None:
+        need = window_mla_workspace_size(T, S, H, q_pos0, sinks, window)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _check(_lib.dsa_window_mla(_p(q), _p(kv), T, S, H, q_pos0, sinks, window, float(sm_scale),
+                               _p(out), _p(lse), _p(_dev(workspace)),
+                               workspace.numel() * workspace.element_size(), _stream(stream)),
+           "dsa_window_mla")
+    return out, lse
+
+
+def attention_mass_paged(q, kv_pool, block_table, seq_len, lse, sm_scale, mass, stream=None):
+    """Adds the attention weight the new tokens give to each cached token to its
+    running total, in place -> mass [B][ld] (a new token's total starts at 0)."""
+    _paged_cache(kv_pool, block_table, seq_len)
+    B, max_blocks = block_table.shape
+    _shaped(q, torch.bfloat16, B, -1, -1, 576)
+    nq, H = q.shape[1], q.shape[2]
+    _shaped(lse, torch.float32, B, nq, H)
+    _shaped(mass, torch.float32, B, -1)
+    _check(_lib.dsa_attention_mass_paged(_p(q), _p(kv_pool), _p(block_table), _p(seq_len), _p(lse),
+                                         B, nq, max_blocks, kv_pool.shape[0], H, float(sm_scale),
+                                         _p(mass), mass.shape[1], _stream(stream)),
+           "dsa_attention_mass_paged")
+    return mass
+
+
+def cache_evict_paged(kv_pool, block_table, seq_len, mass, budget, sinks, recent, k8_pool=None,
+                      k_scale_pool=None, idx=None, seq_len_out=None, mass_out=None, stream=None):
+    """Brings every sequence down to at most `budget` tokens, in place: the first
+    `sinks`, the last `recent` and those of the largest totals -> (idx [B][budget],
+    the new lengths, the moved totals). `seq_len_out` and `mass_out` may be `seq_len`
+    and `mass`; left out, they are new tensors."""
+    _paged_cache(kv_pool, block_table, seq_len)
+    B, max_blocks = block_table.shape
+    nblk, dev = kv_pool.shape[0], kv_pool.device
+    _shaped(mass, torch.float32, B, -1)
+    if k8_pool is not None:
+        k8_pool = _shaped(_u8(k8_pool), torch.uint8, nblk, 64, 128)
+    if k_scale_pool is not None:
+        _shaped(k_scale_pool, torch.float32, nblk, 64)
+    if idx is None:
+        idx = torch.empty(B, max(budget, 0), dtype=torch.int32, device=dev)
+    if seq_len_out is None:
+        seq_len_out = torch.empty_like(seq_len)
+    if mass_out is None:
+        mass_out = torch.zeros_like(mass)
+    _shaped(idx, torch.int32, B, budget)
+    _shaped(seq_len_out, torch.int32, B)
+    _shaped(mass_out, torch.float32, B, -1)
+    _check(_lib.dsa_cache_evict_paged(_p(kv_pool), _p(k8_pool), _p(k_scale_pool), _p(block_table),
+                                      _p(seq_len), _p(mass), mass.shape[1], B, max_blocks, nblk,
+                                      budget, sinks, recent, _p(idx), _p(seq_len_out),
+                                      _p(mass_out), mass_out.shape[1], _stream(stream)),
+           "dsa_cache_evict_paged")
+    return idx, seq_len_out, mass_out
 
 
 def decode_paged_noalloc(q8, q_scale, w, q, k8_pool, k_scale_pool, kv_pool, block_table, seq_len,

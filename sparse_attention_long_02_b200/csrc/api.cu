@@ -417,6 +417,180 @@ int dsa_sparse_mla_decode_paged(const void* q, const void* kv_pool, const int32_
                     block_table, seq_len, max_blocks, nblk, nq, static_cast<cudaStream_t>(stream));
 }
 
+// Checks shared by the calls over ranges of the latent cache. Positions stay
+// below 2^30, so that window and sink arithmetic fits 32 bits, and query rows
+// and cache rows below 2^31 - 128, the coordinates of a tensor map.
+static constexpr long long kMaxPos = 1ll << 30;
+static constexpr long long kMaxMapRows = (1ll << 31) - 128;
+
+static int range_common(RangeArgs& a, const void* q, const void* kv, float sm_scale, void* out,
+                        float* lse, void* workspace, size_t ws_bytes, size_t need,
+                        cudaStream_t st) {
+  if (a.H < 1 || a.H > 128) return DSA_ERR_UNSUPPORTED;
+  const long long queries = a.block_table ? static_cast<long long>(a.B) * a.nq : a.T;
+  if (queries * a.H > kMaxMapRows) return DSA_ERR_INVALID_ARG;
+  if (need && (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+    return DSA_ERR_WORKSPACE;
+  a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.kv = static_cast<const __nv_bfloat16*>(kv);
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = lse;
+  a.err = device_error_word();
+  if (!a.err) return DSA_ERR_CUDA;
+  return status_of(launch_range_mla(a, st));
+}
+
+size_t dsa_window_mla_workspace_size(int T, int S, int H, int q_pos0, int sinks, int window) {
+  (void)T;
+  (void)S;
+  (void)H;
+  (void)q_pos0;
+  (void)sinks;
+  (void)window;
+  return 0;
+}
+
+int dsa_window_mla(const void* q, const void* kv, int T, int S, int H, int q_pos0, int sinks,
+                   int window, float sm_scale, void* out, float* lse, void* workspace,
+                   size_t ws_bytes, dsa_stream_t stream) {
+  if (T == 0) return DSA_OK;
+  if (!q || !kv || !out || T < 0 || S < 1 || q_pos0 < 0 || sinks < 0 || window < 1 ||
+      !(sm_scale > 0.f) || !aligned16(q) || !aligned16(kv) || !aligned16(out) ||
+      static_cast<long long>(q_pos0) + T > kMaxPos || S > kMaxPos)
+    return DSA_ERR_INVALID_ARG;
+  RangeArgs a;
+  a.T = T;
+  a.S = S;
+  a.q_pos0 = q_pos0;
+  a.H = H;
+  a.sinks = static_cast<int>(std::min<long long>(sinks, kMaxPos));
+  a.window = static_cast<int>(std::min<long long>(window, kMaxPos));
+  return range_common(a, q, kv, sm_scale, out, lse, workspace, ws_bytes,
+                      dsa_window_mla_workspace_size(T, S, H, q_pos0, sinks, window),
+                      static_cast<cudaStream_t>(stream));
+}
+
+size_t dsa_split_mla_decode_workspace_size(int B, int nq, int max_blocks, int H) {
+  (void)B;
+  (void)nq;
+  (void)max_blocks;
+  (void)H;
+  return 0;
+}
+
+static int range_decode(const void* q, const void* kv_pool, const int32_t* block_table,
+                        const int32_t* seq_len, int B, int nq, int max_blocks, int nblk, int H,
+                        int sinks, int window, float sm_scale, void* out, float* lse,
+                        void* workspace, size_t ws_bytes, cudaStream_t st) {
+  if (B == 0) return DSA_OK;
+  if (!q || !kv_pool || !block_table || !seq_len || !out || B < 0 || nq < 1 || max_blocks < 1 ||
+      nblk < 1 || !(sm_scale > 0.f) || !aligned16(q) || !aligned16(kv_pool) || !aligned16(out) ||
+      static_cast<long long>(max_blocks) * 64 > kMaxPos || nq > kMaxPos ||
+      static_cast<long long>(nblk) * 64 > kMaxMapRows)
+    return DSA_ERR_INVALID_ARG;
+  RangeArgs a;
+  a.B = B;
+  a.nq = nq;
+  a.H = H;
+  a.sinks = static_cast<int>(std::min<long long>(sinks, kMaxPos));
+  a.window = static_cast<int>(std::min<long long>(window, kMaxPos));
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.nblk = nblk;
+  a.seq_len = seq_len;
+  return range_common(a, q, kv_pool, sm_scale, out, lse, workspace, ws_bytes,
+                      dsa_split_mla_decode_workspace_size(B, nq, max_blocks, H), st);
+}
+
+int dsa_split_mla_decode_paged(const void* q, const void* kv_pool, const int32_t* block_table,
+                               const int32_t* seq_len, int B, int nq, int max_blocks, int nblk,
+                               int H, float sm_scale, void* out, float* lse, void* workspace,
+                               size_t ws_bytes, dsa_stream_t stream) {
+  return range_decode(q, kv_pool, block_table, seq_len, B, nq, max_blocks, nblk, H, 0, 0, sm_scale,
+                      out, lse, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_window_mla_decode_paged(const void* q, const void* kv_pool, const int32_t* block_table,
+                                const int32_t* seq_len, int B, int nq, int max_blocks, int nblk,
+                                int H, int sinks, int window, float sm_scale, void* out,
+                                float* lse, void* workspace, size_t ws_bytes,
+                                dsa_stream_t stream) {
+  if (sinks < 0 || window < 1) return DSA_ERR_INVALID_ARG;
+  return range_decode(q, kv_pool, block_table, seq_len, B, nq, max_blocks, nblk, H, sinks, window,
+                      sm_scale, out, lse, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+}
+
+int dsa_attention_mass_paged(const void* q, const void* kv_pool, const int32_t* block_table,
+                             const int32_t* seq_len, const float* lse, int B, int nq,
+                             int max_blocks, int nblk, int H, float sm_scale, float* mass,
+                             int64_t ld, dsa_stream_t stream) {
+  if (B == 0) return DSA_OK;
+  if (!q || !kv_pool || !block_table || !seq_len || !lse || !mass || B < 0 || nq < 1 ||
+      max_blocks < 1 || nblk < 1 || !(sm_scale > 0.f) || !aligned16(q) || !aligned16(kv_pool) ||
+      static_cast<long long>(max_blocks) * 64 > kMaxPos || nq > kMaxPos ||
+      static_cast<long long>(nblk) * 64 > kMaxMapRows ||
+      ld < static_cast<long long>(max_blocks) * 64)
+    return DSA_ERR_INVALID_ARG;
+  if (H < 1 || H > 128) return DSA_ERR_UNSUPPORTED;
+  if (static_cast<long long>(B) * nq * H > kMaxMapRows) return DSA_ERR_INVALID_ARG;
+  MassArgs a;
+  a.B = B;
+  a.nq = nq;
+  a.H = H;
+  a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.nblk = nblk;
+  a.seq_len = seq_len;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.kv = static_cast<const __nv_bfloat16*>(kv_pool);
+  a.lse = lse;
+  a.mass = mass;
+  a.ld = ld;
+  a.err = device_error_word();
+  if (!a.err) return DSA_ERR_CUDA;
+  return status_of(launch_attention_mass(a, static_cast<cudaStream_t>(stream)));
+}
+
+int dsa_cache_evict_paged(void* kv_pool, void* k8_pool, float* k_scale_pool,
+                          const int32_t* block_table, const int32_t* seq_len, const float* mass,
+                          int64_t ld, int B, int max_blocks, int nblk, int budget, int sinks,
+                          int recent, int32_t* idx, int32_t* seq_len_out, float* mass_out,
+                          int64_t ld_out, dsa_stream_t stream) {
+  if (B == 0) return DSA_OK;
+  if (!kv_pool || !block_table || !seq_len || !mass || !idx || !seq_len_out || B < 0 ||
+      max_blocks < 1 || nblk < 1 || budget < 1 || sinks < 0 || recent < 0 ||
+      static_cast<long long>(sinks) + recent > budget || !aligned16(kv_pool) ||
+      !aligned16(k8_pool) || static_cast<long long>(max_blocks) * 64 > kMaxPos ||
+      ld < static_cast<long long>(max_blocks) * 64 ||
+      (mass_out && ld_out < std::min<long long>(budget, static_cast<long long>(max_blocks) * 64)) ||
+      (mass_out == mass && ld_out != ld))
+    return DSA_ERR_INVALID_ARG;
+  if (B > 65535) return DSA_ERR_UNSUPPORTED;
+  EvictArgs a;
+  a.B = B;
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  a.block_table = block_table;
+  a.max_blocks = max_blocks;
+  a.nblk = nblk;
+  a.seq_len = seq_len;
+  a.mass = mass;
+  a.ld = ld;
+  a.kv_pool = kv_pool;
+  a.k8_pool = k8_pool;
+  a.k_scale_pool = k_scale_pool;
+  a.idx = idx;
+  a.seq_len_out = seq_len_out;
+  a.mass_out = mass_out;
+  a.ld_out = ld_out;
+  a.err = device_error_word();
+  if (!a.err) return DSA_ERR_CUDA;
+  return status_of(launch_cache_evict(a, static_cast<cudaStream_t>(stream)));
+}
+
 // The sparse MLA on a selection this library's top-k wrote: every row holds
 // its selected slots first, so a row that sees fewer than k keys walks only
 // those (rows of a contiguous cache at positions q_pos0 + r).

@@ -131,6 +131,56 @@ struct MlaArgs {
   unsigned* err = nullptr;
 };
 
+// Attention over ranges of the latent cache: every earlier key (window 0), or
+// a sliding window of keys and the first `sinks` ones.
+struct RangeArgs {
+  int T = 0, S = 0, q_pos0 = 0;           // contiguous cache: query rows, keys, first position
+  int B = 0, nq = 1;                      // paged cache: sequences, new queries of each
+  int H = 0, sinks = 0, window = 0;
+  float sm_scale_log2 = 0.f;              // sm_scale * log2(e)
+  const int* block_table = nullptr;       // paged cache or null
+  int max_blocks = 0, nblk = 0;
+  const int* seq_len = nullptr;
+  const __nv_bfloat16* q = nullptr;       // [queries][H][576]
+  const __nv_bfloat16* kv = nullptr;      // [kv rows][576]
+  __nv_bfloat16* out = nullptr;           // [queries][H][512]
+  float* lse = nullptr;                   // [queries][H] or null
+  unsigned* err = nullptr;
+};
+
+// The attention weight the nq new tokens of each sequence give to its cached
+// tokens, added to the running totals mass [B][ld].
+struct MassArgs {
+  int B = 0, nq = 1, H = 0;
+  float sm_scale_log2 = 0.f;
+  const int* block_table = nullptr;
+  int max_blocks = 0, nblk = 0;
+  const int* seq_len = nullptr;
+  const __nv_bfloat16* q = nullptr;       // [B][nq][H][576]
+  const __nv_bfloat16* kv = nullptr;      // [nblk * 64][576]
+  const float* lse = nullptr;             // [B][nq][H]
+  float* mass = nullptr;                  // [B][ld]
+  long long ld = 0;
+  unsigned* err = nullptr;
+};
+
+struct EvictArgs {
+  int B = 0, budget = 0, sinks = 0, recent = 0;
+  const int* block_table = nullptr;
+  int max_blocks = 0, nblk = 0;
+  const int* seq_len = nullptr;
+  const float* mass = nullptr;            // [B][ld]
+  long long ld = 0;
+  void* kv_pool = nullptr;                // [nblk * 64][576] bf16
+  void* k8_pool = nullptr;                // [nblk * 64][128] e4m3 or null
+  float* k_scale_pool = nullptr;          // [nblk * 64] or null
+  int* idx = nullptr;                     // [B][budget] out: the kept slots
+  int* seq_len_out = nullptr;             // [B] out (may be seq_len)
+  float* mass_out = nullptr;              // [B][ld_out] out (may be mass) or null
+  long long ld_out = 0;
+  unsigned* err = nullptr;
+};
+
 // 2D tensor map: `rows` rows of `inner` elements, `row_stride` bytes apart.
 cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
                          uint64_t inner, uint64_t rows, uint64_t row_stride, uint32_t box_inner,
@@ -162,6 +212,10 @@ cudaError_t launch_indexer_backward(const IndexerBwdArgs& a, void* workspace, un
                                     cudaStream_t st);
 cudaError_t launch_sparse_mla(const MlaArgs& a, const void* q, const void* kv, long long kv_rows,
                               long long q_rows, cudaStream_t st);
+
+cudaError_t launch_range_mla(const RangeArgs& a, cudaStream_t st);
+cudaError_t launch_attention_mass(const MassArgs& a, cudaStream_t st);
+cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st);
 
 int indexer_queries_per_cta(int Hi);
 
