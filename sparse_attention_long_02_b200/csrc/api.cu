@@ -84,6 +84,21 @@ cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+cudaError_t make_tmap_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows,
+                             uint32_t box_chunks) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint64_t dims[3] = {64, rows, 9};
+  const cuuint64_t strides[2] = {1152, 128};
+  const cuuint32_t box[3] = {64, box_rows, box_chunks};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+         estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace dsa
 
 using namespace dsa;
@@ -424,11 +439,11 @@ static constexpr long long kMaxPos = 1ll << 30;
 static constexpr long long kMaxMapRows = (1ll << 31) - 128;
 
 static int range_common(RangeArgs& a, const void* q, const void* kv, float sm_scale, void* out,
-                        float* lse, void* workspace, size_t ws_bytes, size_t need,
-                        cudaStream_t st) {
+                        float* lse, void* workspace, size_t ws_bytes, cudaStream_t st) {
   if (a.H < 1 || a.H > 128) return DSA_ERR_UNSUPPORTED;
   const long long queries = a.block_table ? static_cast<long long>(a.B) * a.nq : a.T;
   if (queries * a.H > kMaxMapRows) return DSA_ERR_INVALID_ARG;
+  const size_t need = range_layout(a, workspace);
   if (need && (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
     return DSA_ERR_WORKSPACE;
   a.sm_scale_log2 = sm_scale * 1.4426950408889634f;
@@ -442,13 +457,17 @@ static int range_common(RangeArgs& a, const void* q, const void* kv, float sm_sc
 }
 
 size_t dsa_window_mla_workspace_size(int T, int S, int H, int q_pos0, int sinks, int window) {
-  (void)T;
-  (void)S;
-  (void)H;
-  (void)q_pos0;
-  (void)sinks;
-  (void)window;
-  return 0;
+  if (T <= 0 || S < 1 || H < 1 || H > 128 || q_pos0 < 0 || sinks < 0 || window < 1 ||
+      static_cast<long long>(q_pos0) + T > kMaxPos || S > kMaxPos)
+    return 0;
+  RangeArgs a;
+  a.T = T;
+  a.S = S;
+  a.q_pos0 = q_pos0;
+  a.H = H;
+  a.sinks = static_cast<int>(std::min<long long>(sinks, kMaxPos));
+  a.window = static_cast<int>(std::min<long long>(window, kMaxPos));
+  return range_layout(a, nullptr);
 }
 
 int dsa_window_mla(const void* q, const void* kv, int T, int S, int H, int q_pos0, int sinks,
@@ -467,16 +486,22 @@ int dsa_window_mla(const void* q, const void* kv, int T, int S, int H, int q_pos
   a.sinks = static_cast<int>(std::min<long long>(sinks, kMaxPos));
   a.window = static_cast<int>(std::min<long long>(window, kMaxPos));
   return range_common(a, q, kv, sm_scale, out, lse, workspace, ws_bytes,
-                      dsa_window_mla_workspace_size(T, S, H, q_pos0, sinks, window),
                       static_cast<cudaStream_t>(stream));
 }
 
 size_t dsa_split_mla_decode_workspace_size(int B, int nq, int max_blocks, int H) {
-  (void)B;
-  (void)nq;
-  (void)max_blocks;
-  (void)H;
-  return 0;
+  if (B <= 0 || nq < 1 || max_blocks < 1 || H < 1 || H > 128 ||
+      static_cast<long long>(max_blocks) * 64 > kMaxPos ||
+      static_cast<long long>(B) * nq > kMaxMapRows / H)
+    return 0;
+  static const int paged = 0;              // marks the cache as paged; not read
+  RangeArgs a;
+  a.B = B;
+  a.nq = nq;
+  a.H = H;
+  a.max_blocks = max_blocks;
+  a.block_table = &paged;
+  return range_layout(a, nullptr);
 }
 
 static int range_decode(const void* q, const void* kv_pool, const int32_t* block_table,
@@ -499,8 +524,7 @@ static int range_decode(const void* q, const void* kv_pool, const int32_t* block
   a.max_blocks = max_blocks;
   a.nblk = nblk;
   a.seq_len = seq_len;
-  return range_common(a, q, kv_pool, sm_scale, out, lse, workspace, ws_bytes,
-                      dsa_split_mla_decode_workspace_size(B, nq, max_blocks, H), st);
+  return range_common(a, q, kv_pool, sm_scale, out, lse, workspace, ws_bytes, st);
 }
 
 int dsa_split_mla_decode_paged(const void* q, const void* kv_pool, const int32_t* block_table,

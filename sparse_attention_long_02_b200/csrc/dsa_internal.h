@@ -146,7 +146,18 @@ struct RangeArgs {
   __nv_bfloat16* out = nullptr;           // [queries][H][512]
   float* lse = nullptr;                   // [queries][H] or null
   unsigned* err = nullptr;
+  // work layout (range_layout): row tiles of G queries, `items` of them, over
+  // `clusters` CTA pairs; `whole`: each pair takes whole row tiles
+  int G = 0, per_seq = 0, items = 0, clusters = 0, whole = 0;
+  int rows_pad = 0;                       // rows of a partial result
+  int kv_rows = 0;                        // rows of the kv tensor maps
+  int2* rec = nullptr;                    // workspace [clusters]: split row tile, its last pair
+  float2* part_ml = nullptr;              // workspace [2 * clusters][rows_pad] maxima and sums
+  float4* part_o = nullptr;               // workspace [2 * clusters][128][rows_pad] sums of p v
 };
+// Fills the work layout and the workspace pointers (workspace may be null);
+// returns the workspace bytes.
+size_t range_layout(RangeArgs& a, void* workspace);
 
 // The attention weight the nq new tokens of each sequence give to its cached
 // tokens, added to the running totals mass [B][ld].
@@ -185,6 +196,12 @@ struct EvictArgs {
 cudaError_t make_tmap_2d(CUtensorMap* map, const void* base, CUtensorMapDataType dtype,
                          uint64_t inner, uint64_t rows, uint64_t row_stride, uint32_t box_inner,
                          uint32_t box_rows, CUtensorMapSwizzle swizzle);
+
+// 3D tensor map of bf16 rows of 576 as nine chunks of 64 dims, so that one load
+// of `box_chunks` chunks x `box_rows` rows lands as whole 128-byte-swizzled
+// atoms, one chunk's rows after another.
+cudaError_t make_tmap_chunks(CUtensorMap* map, const void* base, uint64_t rows, uint32_t box_rows,
+                             uint32_t box_chunks);
 
 cudaError_t launch_indexer(const IndexerArgs& a, const void* q8, const void* k8, long long k_rows,
                            cudaStream_t st);

@@ -8,100 +8,957 @@
 //   lse = log sum_s exp(z_s).
 // A row that sees no key gets out = 0 and lse = -inf.
 //
-// One CTA per (query, head): the running maximum and sum of the softmax over
-// blocks of 128 keys, everything in fp32.
+// Row tiles. The MMA's M holds 128 rows: all heads of G = min(queries, 128 / H)
+// consecutive queries of one sequence, which share the keys they read. A row
+// tile's keys are 64-key units (cache blocks) that any of its queries sees,
+// the sinks' units first, then the window's; two units form a tile of 128 keys.
+//
+// Two roles in a cluster of two CTAs. A 128 x 512 fp32 output fills the 512
+// TMEM columns of an SM, so one SM cannot hold it beside the logits. CTA 0
+// forms the logits and the softmax, CTA 1 the output:
+//   CTA 0: K chunks (128 keys x 64 dims) stream through a ring of TMA loads;
+//     S = Q K^T (M = 128, N = 128, K = 576) goes into one of four TMEM
+//     buffers; two groups of four warps (thread = row) take the tiles in
+//     turn: row maximum, running reference maximum (re-based only when it
+//     grows by more than 8 in log2 units), P = exp2(z - m) in bf16 into shared
+//     memory, one 16 KB bulk copy per 64 keys into CTA 1.
+//   CTA 1: V chunks (64 keys x 256 dims) stream through their own ring;
+//     O (+)= P V (M = 128, N = 256 twice, K = 64); eight warps rescale O in
+//     TMEM when a reference maximum moved, and write the result.
+// Nothing below fp32 crosses but P, which the PV product takes in bf16. Both
+// K and V stream from L2 (each 64-key unit is prefetched a few tiles ahead),
+// so neither role waits for the other's loads.
+//
+// Work split. The tiles of all row tiles form one list; each cluster takes an
+// equal share of it, wherever it begins and ends. A row tile inside one share
+// is written directly; one cut over several clusters leaves its parts (fp32
+// sums of p v with the row's maximum and sum) in the workspace, which
+// range_join_kernel combines: with m = max m_i, l = sum l_i 2^(m_i - m),
+// O = sum O_i 2^(m_i - m) / l.
+#include <algorithm>
+
 #include "common.cuh"
 #include "dsa_internal.h"
 
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 384;
+constexpr int kQAtom = 128 * 128;               // 128 rows x 64 dims bf16, 128-B swizzled
+constexpr int kChunk = 128 * 128;               // 128 keys x 64 dims
+constexpr int kUnitChunk = 64 * 128;            // 64 keys x 64 dims
+constexpr int kPAtom = 128 * 128;               // P: 128 rows x 64 keys
+constexpr int kVChunk = 4 * kUnitChunk;         // 64 keys x 256 dims
+constexpr int kKRing = 3;
+constexpr int kSBufs = 4;
+constexpr int kPSlots = 4;
+constexpr int kVRing = 4;
+constexpr int kAhead = 3;                       // tiles of L2 prefetch
+constexpr float kRebase = 8.0f;                 // lazy rescale threshold (log2 units)
+constexpr int kMaxClusters = 74;                // two CTAs on each of 148 SMs
+constexpr int kScanItems = 16384;               // row tiles a cluster scans for its share
+constexpr int kItemCost = 1;                    // a row tile's fixed cost, in tiles
+constexpr int kMinShare = 2;                    // tiles (and fixed costs) a cluster takes at least
 
-// Physical row of key `s`, or -1 when its block id is out of range.
-__device__ __forceinline__ long long key_row(const RangeArgs& A, int b, int s) {
-  if (!A.block_table) return s;
-  const int pb = A.block_table[static_cast<long long>(b) * A.max_blocks + (s >> 6)];
-  if (pb < 0 || pb >= A.nblk) return -1;
-  return static_cast<long long>(pb) * 64 + (s & 63);
-}
+struct LogitsSmem {                             // CTA 0
+  uint8_t q[9][kQAtom];
+  uint8_t k[kKRing][kChunk];
+  uint8_t p[2][kPAtom];                         // each softmax group's staging of P
+};
+struct OutputSmem {                             // CTA 1
+  uint8_t p[kPSlots][kPAtom];
+  uint8_t v[kVRing][kVChunk];
+  float alpha[4][128];                          // rescale factors, by tile
+  float2 ml[2][128];                            // maximum and sum of each softmax group
+};
+constexpr size_t kBig = sizeof(LogitsSmem);
+static_assert(sizeof(OutputSmem) <= kBig && kBig % 1024 == 0, "both roles fit");
 
-__global__ void __launch_bounds__(kThreads) range_mla_kernel(const RangeArgs A) {
-  __shared__ float qs[576], ps[kThreads];
-  __shared__ long long rows[kThreads];
-  __shared__ float red[kThreads / 32];
-  const long long qr = static_cast<long long>(blockIdx.x) / A.H;          // query row
-  const int h = static_cast<int>(blockIdx.x % A.H);
-  const int b = A.block_table ? static_cast<int>(qr / A.nq) : 0;
-  int pos, last;
+struct Ctl {
+  float m[2][128];                              // CTA 0: reference maxima, by tile parity
+  unsigned flag[4][4];                          // CTA 1: [tile][lane quarter] rescale wanted
+  // CTA 0
+  unsigned long long q_full, q_free;
+  unsigned long long k_full[kKRing], k_empty[kKRing];
+  unsigned long long s_full[kSBufs], s_empty[kSBufs];
+  unsigned long long m_bar[4];                  // a tile's reference maxima of a lane quarter
+  // by softmax group, so that whoever waits on one sees every phase of it
+  unsigned long long p_own[2];                  // a staged atom is written
+  unsigned long long p_ack[2];                  // CTA 1 holds the atom: its staging is free
+  unsigned long long p_room[kPSlots];           // CTA 1 has room for another atom
+  unsigned long long ml_free;                   // CTA 1 has read ml
+  // CTA 1
+  unsigned long long v_full[kVRing], v_empty[kVRing];
+  unsigned long long p_full[kPSlots], p_free[kPSlots];
+  unsigned long long al_full[4];                // a tile's rescale factors have landed
+  unsigned long long o_ok[4];                   // O and V are ready for a tile's PV
+  unsigned long long pv_done[4];
+  unsigned long long o_done;
+  unsigned long long ml_full;
+  // the cluster's share of the work
+  long long total, start;                       // all weight; the weight before the share
+  int item, off, left, nc;                      // first row tile, offset into it, weight, clusters
+  uint32_t tmem_base;
+  int abort_flag;
+};
+constexpr size_t kSmemBytes = kBig + sizeof(Ctl) + 1024;
+static_assert(kSmemBytes <= 232448, "fits the 227 KB of shared memory a CTA may use");
+
+// A row tile: its rows, positions and 64-key units.
+struct Item {
+  long long row0;                               // first row of q, out and lse
+  int nrows;
+  int pos0, posl;                               // positions of its first and last query
+  int last;                                     // last key of the sequence
+  int ns, w0, nu;                               // units: 0 .. ns-1, then w0 on; nu in all
+  int tiles;                                    // of two units, at least one
+  const int* table;                             // the sequence's block table (paged)
+};
+
+__device__ __forceinline__ Item item_geom(const RangeArgs& A, int i) {
+  Item x;
+  int nq;
   if (A.block_table) {
-    const int len = A.seq_len[b], cap = A.max_blocks * 64;
-    if (threadIdx.x == 0 && (len < 0 || len > cap)) raise_error(A.err, kErrBounds);
-    last = max(0, min(len, cap)) - 1;
-    pos = last + 1 - A.nq + static_cast<int>(qr % A.nq);
+    const int b = i / A.per_seq, j0 = (i - b * A.per_seq) * A.G;
+    nq = min(A.G, A.nq - j0);
+    const int len = max(0, min(A.seq_len[b], A.max_blocks * 64));
+    x.pos0 = len - A.nq + j0;
+    x.last = len - 1;
+    x.row0 = (static_cast<long long>(b) * A.nq + j0) * A.H;
+    x.table = A.block_table + static_cast<long long>(b) * A.max_blocks;
   } else {
-    last = A.S - 1;
-    pos = A.q_pos0 + static_cast<int>(qr);
+    const int j0 = i * A.G;
+    nq = min(A.G, A.T - j0);
+    x.pos0 = A.q_pos0 + j0;
+    x.last = A.S - 1;
+    x.row0 = static_cast<long long>(j0) * A.H;
+    x.table = nullptr;
   }
-  const int hi = min(pos, last);
-  const int lo = A.window ? max(0, pos - A.window + 1) : 0;
-  const int ns = A.window ? min(min(A.sinks, lo), hi + 1) : 0;            // sinks before the window
-  const int n = max(0, ns) + max(0, hi - lo + 1);
-  const __nv_bfloat16* q = A.q + (qr * A.H + h) * 576;
-  for (int i = threadIdx.x; i < 576; i += kThreads) qs[i] = __bfloat162float(q[i]);
-  __syncthreads();
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k0 = 0; k0 < n; k0 += kThreads) {
-    const int i = k0 + threadIdx.x;
-    float z = -INFINITY;
-    long long r = -1;
-    if (i < n) {
-      r = key_row(A, b, i < ns ? i : lo + i - ns);
-      if (r < 0) {
-        raise_error(A.err, kErrBounds);
-      } else {
-        const __nv_bfloat16* k = A.kv + r * 576;
-        float s = 0.f;
-        for (int d = 0; d < 576; ++d) s += qs[d] * __bfloat162float(k[d]);
-        z = s * A.sm_scale_log2;
+  x.nrows = nq * A.H;
+  x.posl = x.pos0 + nq - 1;
+  const int hi = min(x.posl, x.last);
+  const int lo = A.window ? max(0, x.pos0 - A.window + 1) : 0;
+  int w1 = 0;
+  x.ns = x.w0 = 0;
+  if (hi >= 0) {
+    if (lo <= hi) {
+      x.w0 = lo >> 6;
+      w1 = (hi >> 6) + 1;
+    }
+    if (A.window && A.sinks) {
+      x.ns = (min(A.sinks, hi + 1) + 63) >> 6;
+      if (w1 == 0) {
+        x.w0 = w1 = x.ns;
+      } else if (x.ns >= x.w0) {
+        x.ns = x.w0 = 0;
       }
     }
-    float t = z;
-#pragma unroll
-    for (int w = 16; w > 0; w >>= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, w));
-    if (lane_id() == 0) red[warp_id()] = t;
-    __syncthreads();
-    t = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float mn = fmaxf(m, t);
-    const float base = mn == -INFINITY ? 0.f : mn;
-    const float alpha = exp2f(m - base);
-    const float p = r < 0 ? 0.f : exp2f(z - base);
-    rows[threadIdx.x] = r;
-    ps[threadIdx.x] = p;
-    __syncthreads();
-    l *= alpha;
-    for (int e = 0; e < 4; ++e) o[e] *= alpha;
-    for (int j = 0; j < min(kThreads, n - k0); ++j) {
-      l += ps[j];
-      if (rows[j] < 0) continue;
-      const __nv_bfloat16* v = A.kv + rows[j] * 576 + 4 * threadIdx.x;
-      for (int e = 0; e < 4; ++e) o[e] += ps[j] * __bfloat162float(v[e]);
+  }
+  x.nu = x.ns + w1 - x.w0;
+  x.tiles = max(1, (x.nu + 1) >> 1);
+  return x;
+}
+
+__device__ __forceinline__ int unit_block(const Item& x, int u) {
+  return u < x.ns ? u : x.w0 + u - x.ns;
+}
+__device__ __forceinline__ int tile_units(const Item& x, int t) {
+  return x.nu - 2 * t >= 2 ? 2 : 1;
+}
+// Cache row of unit u's first key, or kv_rows (whose loads give zeros) when
+// the row tile has no keys or the block id is out of range.
+__device__ __forceinline__ int unit_row(const RangeArgs& A, const Item& x, int u) {
+  if (u >= x.nu) return A.kv_rows;
+  const int block = unit_block(x, u);
+  if (!A.block_table) return block * 64;
+  const int pb = __ldg(x.table + block);
+  return pb < 0 || pb >= A.nblk ? A.kv_rows : pb * 64;
+}
+
+// A cluster's share, one piece (tiles [t0, t1) of a row tile) after another.
+// Every warp walks it on its own; all see the same pieces.
+struct Piece {
+  int item, t0, t1;
+  bool first, last;                             // holds the row tile's first, last tile
+  long long start;                              // the row tile's place in the weight list
+};
+struct Walk {
+  int item, off, left;
+  long long start;
+  __device__ __forceinline__ Walk(const Ctl& c)
+      : item(c.item), off(c.off), left(c.left), start(c.start) {}
+  __device__ __forceinline__ bool next(const RangeArgs& A, Piece& p, Item& x) {
+    if (A.whole) {
+      // later rows of a prefill see more keys: they go first
+      if (item >= A.items) return false;
+      p.item = A.items - 1 - item;
+      item += A.clusters;
+      x = item_geom(A, p.item);
+      p.t0 = 0;
+      p.t1 = x.tiles;
+      p.first = p.last = true;
+      return true;
     }
-    m = mn;
-    __syncthreads();
+    while (left > 0 && item < A.items) {
+      x = item_geom(A, item);
+      const int weight = x.tiles + kItemCost;
+      const int take = min(weight - off, left);
+      p.item = item;
+      p.t0 = max(0, off - kItemCost);
+      p.t1 = off + take - kItemCost;
+      p.start = start;
+      p.first = p.t0 == 0;
+      p.last = p.t1 == x.tiles;
+      left -= take;
+      off = 0;
+      start += weight;
+      ++item;
+      if (p.t1 > p.t0) return true;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ long long share_begin(long long total, int nc, int c) {
+  return total * c / nc;
+}
+
+// Finds this cluster's share: the weights of all row tiles are added up and
+// cut into equal parts. `sums` is scratch for one number a thread.
+__device__ void find_share(const RangeArgs& A, Ctl& ctl, long long* sums, int cluster) {
+  const int tid = static_cast<int>(threadIdx.x);
+  if (A.whole) {
+    if (tid == 0) {
+      ctl.item = cluster;
+      ctl.off = ctl.left = 0;
+      ctl.start = 0;
+    }
+    return;
+  }
+  const int per = (A.items + kThreads - 1) / kThreads;
+  const int i0 = min(A.items, tid * per), i1 = min(A.items, i0 + per);
+  long long sum = 0;
+  for (int i = i0; i < i1; ++i) {
+    if (A.block_table && blockIdx.x == 0) {
+      const int len = A.seq_len[i / A.per_seq];
+      if (len < 0 || len > A.max_blocks * 64) raise_error(A.err, kErrBounds);
+    }
+    sum += item_geom(A, i).tiles + kItemCost;
+  }
+  sums[tid] = sum;
+  if (tid == 0) {
+    ctl.item = A.items;
+    ctl.off = ctl.left = 0;
+    ctl.start = 0;
+  }
+  __syncthreads();
+  if (tid < 32) {
+    long long mine = 0;
+    for (int k = 0; k < kThreads / 32; ++k) mine += sums[tid * (kThreads / 32) + k];
+    long long before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, before, o);
+      if (tid >= o) before += y;
+    }
+    if (tid == 31) ctl.total = before;
+    before -= mine;
+    for (int k = 0; k < kThreads / 32; ++k) {
+      const long long v = sums[tid * (kThreads / 32) + k];
+      sums[tid * (kThreads / 32) + k] = before;
+      before += v;
+    }
+  }
+  __syncthreads();
+  const long long total = ctl.total;
+  const int nc = static_cast<int>(
+      max(1ll, min(static_cast<long long>(A.clusters), total / kMinShare)));
+  if (tid == 0) ctl.nc = nc;
+  if (cluster >= nc) return;
+  const long long w0 = share_begin(total, nc, cluster), w1 = share_begin(total, nc, cluster + 1);
+  if (sums[tid] <= w0 && w0 < sums[tid] + sum) {
+    long long at = sums[tid];
+    for (int i = i0; i < i1; ++i) {
+      const int weight = item_geom(A, i).tiles + kItemCost;
+      if (w0 < at + weight) {
+        ctl.item = i;
+        ctl.off = static_cast<int>(w0 - at);
+        ctl.left = static_cast<int>(w1 - w0);
+        ctl.start = at;
+        break;
+      }
+      at += weight;
+    }
+  }
+}
+
+// Bits of the 64 keys from kb on that a row with positions [lo, hi] and the
+// first `sinks` keys sees.
+__device__ __forceinline__ unsigned long long range_bits(int a, int b) {
+  a = max(a, 0);
+  b = min(b, 63);
+  if (a > b) return 0ull;
+  return (~0ull >> (63 - b)) & (~0ull << a);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const RangeArgs A) {
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* big = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                            ~static_cast<uintptr_t>(1023));
+  LogitsSmem& sl = *reinterpret_cast<LogitsSmem*>(big);
+  OutputSmem& so = *reinterpret_cast<OutputSmem*>(big);
+  Ctl& ctl = *reinterpret_cast<Ctl*>(big + kBig);
+  unsigned* err = A.err;
+  const uint32_t rank = cluster_rank(), peer = rank ^ 1u;
+  const int cluster = static_cast<int>(blockIdx.x >> 1);
+  const int warp = warp_id(), lane = lane_id();
+
+  find_share(A, ctl, reinterpret_cast<long long*>(big), cluster);
+  if (threadIdx.x == 0) {
+    auto init = [](unsigned long long& b, int count) { mbar_init(smem_u32(&b), count); };
+    init(ctl.q_full, 1);
+    init(ctl.q_free, 1);
+    for (int i = 0; i < kKRing; ++i) {
+      init(ctl.k_full[i], 1);
+      init(ctl.k_empty[i], 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      init(ctl.s_full[i], 1);
+      init(ctl.s_empty[i], 4);
+      init(ctl.m_bar[i], 1);
+      init(ctl.p_room[i], 1);
+      init(ctl.v_full[i], 1);
+      init(ctl.v_empty[i], 1);
+      init(ctl.p_full[i], 1);
+      init(ctl.p_free[i], 1);
+      init(ctl.al_full[i], 4);
+      init(ctl.o_ok[i], 8);
+      init(ctl.pv_done[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      init(ctl.p_own[i], 4);
+      init(ctl.p_ack[i], 1);
+    }
+    init(ctl.ml_free, 8);
+    init(ctl.o_done, 1);
+    init(ctl.ml_full, 8);
+    ctl.abort_flag = launch_aborted(err) ? 1 : 0;
+    fence_barrier_init();
+    // CTA 1 expects the first atoms of P before CTA 0 can send one
+    if (rank == 1)
+      for (int i = 0; i < kPSlots; ++i) mbar_expect_tx(smem_u32(&ctl.p_full[i]), kPAtom);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), 512);
+    tmem_relinquish();
+  }
+  fence_proxy_async_smem();               // find_share's scratch, before loads land there
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();          // barriers of both CTAs initialised before any remote arrive
+  tc_fence_after();
+  const uint32_t tmem = ctl.tmem_base;
+  volatile int* abort_flag = &ctl.abort_flag;
+  Walk walk(ctl);
+  Piece p;
+  Item x;
+  bool ok = *abort_flag == 0;
+
+  if (rank == 0) {
+    if (warp == 0 || warp == 2) {
+      // ------------------------------------------------ Q and K loads (CTA 0)
+      // Two warps take the K chunks in turn: a wait, an expect and a load cost
+      // one thread about 360 cycles, a chunk's MMAs only 274.
+      const int par = warp >> 1;
+      if (lane == 0) {
+        int kc = 0, pieces = 0;
+        const uint32_t qf = smem_u32(&ctl.q_full);
+        while (ok && walk.next(A, p, x)) {
+          if (par == 0) {
+            if (pieces > 0 &&
+                !(ok = mbar_wait(smem_u32(&ctl.q_free), (pieces - 1) & 1, abort_flag, err)))
+              break;
+            mbar_expect_tx(qf, 9 * kQAtom);
+            for (int a = 0; a < 9; ++a)
+              tma_load_2d(smem_u32(sl.q[a]), &tm_q, qf, 64 * a, static_cast<int>(x.row0));
+          }
+          auto prefetch_tile = [&](int t) {
+            if (t >= p.t1) return;
+            for (int u = 2 * t; u < min(2 * t + 2, x.nu); ++u) {
+              const int row = unit_row(A, x, u);
+              if (row < A.kv_rows)
+                prefetch_l2(A.kv + static_cast<long long>(row) * 576,
+                            1152u * static_cast<unsigned>(min(64, A.kv_rows - row)));
+            }
+          };
+          if (par == 0)
+            for (int t = 1; t < kAhead; ++t) prefetch_tile(p.t0 + t);
+          int r0 = unit_row(A, x, 2 * p.t0), r1 = unit_row(A, x, 2 * p.t0 + 1);
+          for (int t = p.t0; ok && t < p.t1; ++t) {
+            const int n = tile_units(x, t);
+            const int c0 = r0, c1 = r1;
+            r0 = unit_row(A, x, 2 * t + 2);
+            r1 = unit_row(A, x, 2 * t + 3);
+            if (par == 0) prefetch_tile(t + kAhead);
+            for (int ch = 0; ch < 9; ++ch, ++kc) {
+              if ((kc & 1) != par) continue;
+              const int st = kc % kKRing;
+              if (kc >= kKRing && !(ok = mbar_wait(smem_u32(&ctl.k_empty[st]),
+                                                   (kc / kKRing + 1) & 1, abort_flag, err)))
+                break;
+              const uint32_t full = smem_u32(&ctl.k_full[st]);
+              mbar_expect_tx(full, n * kUnitChunk);
+              tma_load_3d(smem_u32(sl.k[st]), &tm_k, full, 0, c0, ch);
+              if (n > 1) tma_load_3d(smem_u32(sl.k[st] + kUnitChunk), &tm_k, full, 0, c1, ch);
+            }
+          }
+          ++pieces;
+        }
+        if (!ok) {           // let the loads in flight land before this CTA leaves
+          for (int c = max(0, kc - kKRing); c < kc; ++c)
+            if ((c & 1) == par) mbar_drain(smem_u32(&ctl.k_full[c % kKRing]), (c / kKRing) & 1);
+          if (par == 0 && pieces >= 0) mbar_drain(qf, pieces & 1);
+        }
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------- QK (CTA 0)
+      const uint32_t id2 = idesc_bf16(128, 128, false), id1 = idesc_bf16(128, 64, false);
+      int kc = 0, tc = 0, pieces = 0;
+      // debug: ml_free completes only after an output is written, so this
+      // bounded wait runs out and both CTAs leave through their give-up paths
+      if (ok && (debug_bits(err) & kDbgStallMla))
+        ok = warp_wait(smem_u32(&ctl.ml_free), 0, abort_flag, err);
+      while (ok && walk.next(A, p, x)) {
+        if (!(ok = warp_wait(smem_u32(&ctl.q_full), pieces & 1, abort_flag, err))) break;
+        for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
+          const int sb = tc & 3;
+          if (tc >= kSBufs &&
+              !(ok = warp_wait(smem_u32(&ctl.s_empty[sb]), ((tc >> 2) + 1) & 1, abort_flag, err)))
+            break;
+          tc_fence_after();
+          const uint32_t d = tmem + 128 * sb;
+          const uint32_t id = tile_units(x, t) > 1 ? id2 : id1;
+          for (int ch = 0; ch < 9; ++ch, ++kc) {
+            const int st = kc % kKRing;
+            if (!(ok = warp_wait(smem_u32(&ctl.k_full[st]), (kc / kKRing) & 1, abort_flag, err)))
+              break;
+            if (elect_one()) {
+              const uint64_t qd = sdesc_sw128(smem_u32(sl.q[ch]), 0, 1024);
+              const uint64_t kd = sdesc_sw128(smem_u32(sl.k[st]), 0, 1024);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16(d, qd + 2 * kk, kd + 2 * kk, id, (ch > 0 || kk > 0) ? 1u : 0u);
+              mma_commit(smem_u32(&ctl.k_empty[st]));
+              if (ch == 8) {
+                mma_commit(smem_u32(&ctl.s_full[sb]));
+                if (t + 1 == p.t1) mma_commit(smem_u32(&ctl.q_free));
+              }
+            }
+            __syncwarp();
+          }
+        }
+        ++pieces;
+      }
+      if (!ok) {             // MMAs in flight read shared memory: wait for them
+        if (elect_one()) {
+          mma_commit(smem_u32(&ctl.o_done));
+          mbar_drain(smem_u32(&ctl.o_done), 0);
+        }
+        __syncwarp();
+      }
+    } else if (warp == 3) {
+      // ----------------------------------------------- P to CTA 1 (CTA 0)
+      if (lane == 0) {
+        int a = 0, tc = 0, sent[2] = {0, 0};
+        while (ok && walk.next(A, p, x)) {
+          for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
+            const int g = tc & 1;
+            for (int u = tile_units(x, t); ok && u > 0; --u, ++a) {
+              const int slot = a & 3;
+              if (!(ok = mbar_wait(smem_u32(&ctl.p_own[g]), sent[g] & 1, abort_flag, err))) break;
+              if (a >= kPSlots && !(ok = mbar_wait<true>(smem_u32(&ctl.p_room[slot]),
+                                                         ((a >> 2) + 1) & 1, abort_flag, err)))
+                break;
+              bulk_copy_to_peer(mapa(smem_u32(so.p[slot]), peer), smem_u32(sl.p[g]), kPAtom,
+                                mapa(smem_u32(&ctl.p_full[slot]), peer));
+              ++sent[g];
+            }
+          }
+        }
+        // a copy reads this CTA's staging until it lands
+        for (int g = 0; g < 2; ++g) {
+          if (sent[g] == 0) continue;
+          const uint32_t bar = smem_u32(&ctl.p_ack[g]), parity = (sent[g] - 1) & 1;
+          if (!mbar_wait<true>(bar, parity, abort_flag, err)) mbar_drain(bar, parity);
+        }
+      }
+    } else {
+      // -------------------------------------------------- softmax (CTA 0)
+      const int g = (warp - 4) >> 2;                    // takes the tiles of its parity
+      const int wq = warp & 3;                          // TMEM lane quarter
+      const int r = 32 * wq + lane;                     // row = TMEM lane
+      const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
+      int tc = 0, atoms = 0, pieces = 0;
+      while (ok && walk.next(A, p, x)) {
+        const int pos = x.pos0 + r / A.H;
+        const int hi = r < x.nrows ? min(pos, x.last) : -1;
+        const int lo = A.window ? pos - A.window + 1 : 0;
+        const int sink_hi = A.window ? min(A.sinks - 1, hi) : -1;
+        float m_own = -INFINITY, l = 0.f;
+        for (int t = p.t0; ok && t < p.t1; ++t) {
+          const int n = tile_units(x, t);
+          if ((tc & 1) == g) {
+            const int sb = tc & 3;
+            unsigned long long vis[2] = {0ull, 0ull};
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int un = 2 * t + u;
+              if (un >= x.nu) continue;
+              const int block = unit_block(x, un);
+              bool good = true;
+              if (A.block_table) {
+                const int pb = __ldg(x.table + block);
+                good = pb >= 0 && pb < A.nblk;
+                if (!good && lane == 0) raise_error(err, kErrBounds);
+              }
+              const int kb = block * 64;
+              if (good) vis[u] = range_bits(lo - kb, hi - kb) | range_bits(0, sink_hi - kb);
+            }
+            if (!(ok = warp_wait(smem_u32(&ctl.s_full[sb]), (tc >> 2) & 1, abort_flag, err))) break;
+            tc_fence_after();
+            const uint32_t s_cols = tmem + lanes + 128 * sb;
+            float mx = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (u >= n) continue;
+              float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+              float s[64];
+              tmem_ld64(s_cols + 64 * u, s);
+              if (__all_sync(0xffffffffu, vis[u] == ~0ull)) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) pm[e & 3] = fmaxf(pm[e & 3], s[e]);
+              } else {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                  pm[e & 3] = fmaxf(pm[e & 3], (vis[u] >> e) & 1ull ? s[e] : -INFINITY);
+              }
+              mx = fmaxf(mx, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));
+            }
+            mx *= A.sm_scale_log2;
+            // the other group's reference maximum of the tile before
+            if (tc > 0 &&
+                !(ok = warp_wait(smem_u32(&ctl.m_bar[wq]), (tc - 1) & 1, abort_flag, err)))
+              break;
+            const bool first = t == p.t0;
+            const float m_prev = first ? -INFINITY : ctl.m[(tc + 1) & 1][r];
+            const float m_new = mx > m_prev + kRebase ? mx : m_prev;
+            ctl.m[tc & 1][r] = m_new;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.m_bar[wq]));
+            const bool re = m_prev > -INFINITY && m_new != m_prev;
+            const bool any = __any_sync(0xffffffffu, re);
+            if (m_own > -INFINITY && m_own != m_new) l *= fast_exp2(m_own - m_new);
+            m_own = m_new;
+            const float base = m_new == -INFINITY ? 0.f : m_new;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (u >= n) continue;
+              float s[64];
+              tmem_ld64(s_cols + 64 * u, s);
+              if (u + 1 == n) {                         // the buffer is free for another tile
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl.s_empty[sb]));
+              }
+              float ps[4] = {0.f, 0.f, 0.f, 0.f};
+              uint32_t pk[32];
+              if (__all_sync(0xffffffffu, vis[u] == ~0ull)) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e) s[e] = fast_exp2(fmaf(s[e], A.sm_scale_log2, -base));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                  s[e] = (vis[u] >> e) & 1ull ? fast_exp2(fmaf(s[e], A.sm_scale_log2, -base)) : 0.f;
+              }
+#pragma unroll
+              for (int e = 0; e < 32; ++e) {
+                ps[e & 3] += s[2 * e] + s[2 * e + 1];
+                const __nv_bfloat162 pb = __floats2bfloat162_rn(s[2 * e], s[2 * e + 1]);
+                pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
+              }
+              l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+              if (atoms > 0 && !(ok = warp_wait<true>(smem_u32(&ctl.p_ack[g]), (atoms - 1) & 1,
+                                                      abort_flag, err)))
+                break;
+              ++atoms;
+              if (u == 0) {
+                // Rescale factors of this tile tc, in the slot of tile tc - 4.
+                // CTA 1 has read that one: the last atom of tile tc - 2 has
+                // landed there (the wait above), in the place of the atom
+                // four before, which PV freed after its tile's rescale and
+                // which is tile tc - 4's or later, unless tiles tc - 3 and
+                // tc - 2 both ended a piece; then ml_free has let this warp
+                // pass only after CTA 1 was done with tile tc - 3.
+                if (any) st_cluster_f32(mapa(smem_u32(&so.alpha[tc & 3][r]), peer),
+                                        re ? fast_exp2(m_prev - m_new) : 1.f);
+                if (lane == 0)
+                  st_cluster_f32(mapa(smem_u32(&ctl.flag[tc & 3][wq]), peer),
+                                 __uint_as_float(any ? 1u : 0u));
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctl.al_full[tc & 3]), peer));
+              }
+              // row r of the atom: 128 B, 16-B chunk c at chunk c ^ (r % 8)
+              uint4* row = reinterpret_cast<uint4*>(sl.p[g] + r * 128);
+#pragma unroll
+              for (int c = 0; c < 8; ++c)
+                row[c ^ (r & 7)] =
+                    make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+              fence_proxy_async_smem();                 // generic writes -> bulk-copy reads
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&ctl.p_own[g]));
+            }
+          }
+          ++tc;
+        }
+        if (!ok) break;
+        // the group's maximum and sum go to CTA 1
+        if (pieces > 0 && !(ok = warp_wait<true>(smem_u32(&ctl.ml_free), (pieces - 1) & 1,
+                                                 abort_flag, err)))
+          break;
+        const uint32_t ml = mapa(smem_u32(&so.ml[g][r]), peer);
+        st_cluster_f32(ml, m_own);
+        st_cluster_f32(ml + 4, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctl.ml_full), peer));
+        ++pieces;
+      }
+    }
+  } else {
+    if (warp == 0) {
+      // ---------------------------------------------------- V loads (CTA 1)
+      if (lane == 0) {
+        int vc = 0;
+        while (ok && walk.next(A, p, x)) {
+          int r0 = unit_row(A, x, 2 * p.t0), r1 = unit_row(A, x, 2 * p.t0 + 1);
+          for (int t = p.t0; ok && t < p.t1; ++t) {
+            const int n = tile_units(x, t);
+            const int c0 = r0, c1 = r1;
+            r0 = unit_row(A, x, 2 * t + 2);
+            r1 = unit_row(A, x, 2 * t + 3);
+            for (int h = 0; h < 2 * n; ++h, ++vc) {
+              const int st = vc & 3;
+              if (vc >= kVRing && !(ok = mbar_wait(smem_u32(&ctl.v_empty[st]), ((vc >> 2) + 1) & 1,
+                                                   abort_flag, err)))
+                break;
+              const uint32_t full = smem_u32(&ctl.v_full[st]);
+              mbar_expect_tx(full, kVChunk);
+              tma_load_3d(smem_u32(so.v[st]), &tm_v, full, 0, h < 2 ? c0 : c1, 4 * (h & 1));
+            }
+          }
+        }
+        if (!ok)
+          for (int c = max(0, vc - kVRing); c < vc; ++c)
+            mbar_drain(smem_u32(&ctl.v_full[c & 3]), (c >> 2) & 1);
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------- PV (CTA 1)
+      const uint32_t id = idesc_bf16(128, 256, true);
+      int vc = 0, tc = 0, ac = 0;
+      while (ok && walk.next(A, p, x)) {
+        for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
+          const int n = tile_units(x, t);
+          if (!(ok = warp_wait(smem_u32(&ctl.o_ok[tc & 3]), (tc >> 2) & 1, abort_flag, err))) break;
+          tc_fence_after();
+          for (int u = 0; ok && u < n; ++u, ++ac) {
+            const int slot = ac & 3;
+            if (!(ok = warp_wait<true>(smem_u32(&ctl.p_full[slot]), (ac >> 2) & 1, abort_flag,
+                                       err)))
+              break;
+            for (int h = 0; h < 2; ++h, ++vc) {
+              const int st = vc & 3;
+              if (!(ok = warp_wait(smem_u32(&ctl.v_full[st]), (vc >> 2) & 1, abort_flag, err)))
+                break;
+              if (elect_one()) {
+                const uint64_t pd = sdesc_sw128(smem_u32(so.p[slot]), 0, 1024);
+                const uint64_t vd = sdesc_sw128(smem_u32(so.v[st]), kUnitChunk, 1024);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)          // 16 keys: 32 B of P, 2 KB of V
+                  mma_bf16(tmem + 256 * h, pd + 2 * kk, vd + (kk * 2048 >> 4), id,
+                           (t > p.t0 || u > 0 || kk > 0) ? 1u : 0u);
+                mma_commit(smem_u32(&ctl.v_empty[st]));
+                if (h == 1) {
+                  mma_commit(smem_u32(&ctl.p_free[slot]));
+                  if (u + 1 == n) {
+                    mma_commit(smem_u32(&ctl.pv_done[tc & 3]));
+                    if (t + 1 == p.t1) mma_commit(smem_u32(&ctl.o_done));
+                  }
+                }
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+      if (!ok) {
+        if (elect_one()) {
+          mma_commit(smem_u32(&ctl.q_full));
+          mbar_drain(smem_u32(&ctl.q_full), 0);
+        }
+        __syncwarp();
+      }
+    } else if (warp == 2 || warp == 3) {
+      // ---- word to CTA 0: an atom has landed (warp 2), its slot is free (warp 3)
+      if (lane == 0) {
+        int a = 0, tc = 0;
+        while (ok && walk.next(A, p, x)) {
+          for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
+            for (int u = tile_units(x, t); ok && u > 0; --u, ++a) {
+              const int slot = a & 3;
+              if (warp == 2) {
+                if (!(ok = mbar_wait<true>(smem_u32(&ctl.p_full[slot]), (a >> 2) & 1, abort_flag,
+                                           err)))
+                  break;
+                mbar_arrive_remote(mapa(smem_u32(&ctl.p_ack[tc & 1]), peer));
+              } else {
+                if (!(ok = mbar_wait(smem_u32(&ctl.p_free[slot]), (a >> 2) & 1, abort_flag, err)))
+                  break;
+                mbar_expect_tx(smem_u32(&ctl.p_full[slot]), kPAtom);
+                mbar_arrive_remote(mapa(smem_u32(&ctl.p_room[slot]), peer));
+              }
+            }
+          }
+        }
+      }
+    } else {
+      // ------------------------------------- rescale and output (CTA 1)
+      const int g = (warp - 4) >> 2;                    // half of the 512 value dims
+      const int wq = warp & 3;
+      const int r = 32 * wq + lane;
+      const uint32_t o_cols = tmem + (static_cast<uint32_t>(32 * wq) << 16) + 256 * g;
+      int tc = 0, vc = 0, pieces = 0;
+      bool recorded = false;
+      while (ok && walk.next(A, p, x)) {
+        for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
+          const int n = tile_units(x, t);
+          const int sl4 = tc & 3;
+          // a tile some row does not see whole: its P holds zeros, and a zero
+          // times a NaN or infinite value would reach that row
+          bool edge = false;
+          for (int u = 2 * t; u < min(2 * t + n, x.nu); ++u) {
+            const int kb = unit_block(x, u) * 64;
+            edge |= kb + 63 > min(x.pos0, x.last) ||
+                    (A.window && kb < x.posl - A.window + 1 && kb + 63 >= A.sinks);
+          }
+          // (every tile's chunks are waited for, so that no phase is missed)
+          for (int c = vc; ok && c < vc + 2 * n; ++c) {
+            if (!(ok = warp_wait(smem_u32(&ctl.v_full[c & 3]), (c >> 2) & 1, abort_flag, err)))
+              break;
+            if (edge) {
+              uint4* v = reinterpret_cast<uint4*>(so.v[c & 3]);
+              auto clean = [](uint32_t w) {
+                if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+                if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+                return w;
+              };
+              for (int i = threadIdx.x - 128; i < kVChunk / 16; i += 256) {
+                const uint4 o = v[i];
+                const uint4 w = make_uint4(clean(o.x), clean(o.y), clean(o.z), clean(o.w));
+                if (w.x != o.x || w.y != o.y || w.z != o.z || w.w != o.w) v[i] = w;
+              }
+            }
+          }
+          if (!ok) break;
+          if (edge) fence_proxy_async_smem();
+          vc += 2 * n;
+          if (!(ok = warp_wait<true>(smem_u32(&ctl.al_full[sl4]), (tc >> 2) & 1, abort_flag, err)))
+            break;
+          if (ctl.flag[sl4][wq]) {
+            const float alpha = so.alpha[sl4][r];
+            // never on a piece's first tile, so the PV of the tile before is this piece's
+            if (!(ok = warp_wait(smem_u32(&ctl.pv_done[(tc + 3) & 3]), ((tc - 1) >> 2) & 1,
+                                 abort_flag, err)))
+              break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < 8; ++cc) {
+              float o[32];
+              tmem_ld32(o_cols + 32 * cc, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= alpha;
+              tmem_st32(o_cols + 32 * cc, o);
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.o_ok[sl4]));
+        }
+        if (!ok) break;
+        // ------------------------------------------------------- a piece's end
+        if (!(ok = warp_wait<true>(smem_u32(&ctl.ml_full), pieces & 1, abort_flag, err))) break;
+        const float2 a0 = so.ml[0][r], a1 = so.ml[1][r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctl.ml_free), peer));
+        const float m = fmaxf(a0.x, a1.x);
+        const float l = (a0.x > -INFINITY ? a0.y * fast_exp2(a0.x - m) : a0.y) +
+                        (a1.x > -INFINITY ? a1.y * fast_exp2(a1.x - m) : a1.y);
+        if (!(ok = warp_wait(smem_u32(&ctl.o_done), pieces & 1, abort_flag, err))) break;
+        tc_fence_after();
+        const bool valid = r < x.nrows;
+        if (p.first && p.last) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          __nv_bfloat16* orow = A.out + (x.row0 + r) * 512 + 256 * g;
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {
+            float o[32];
+            tmem_ld32(o_cols + 32 * cc, o);
+            if (!valid) continue;
+            uint4* dst = reinterpret_cast<uint4*>(orow + 32 * cc);
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              uint32_t w[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * q4 + 2 * e] * inv,
+                                                               o[8 * q4 + 2 * e + 1] * inv);
+                w[e] = *reinterpret_cast<const uint32_t*>(&v);
+              }
+              dst[q4] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (g == 0 && valid && A.lse)
+            A.lse[x.row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+        } else {
+          // one of the parts of a cut row tile: slot 1 of the cluster that
+          // holds its first tile, slot 0 of the others
+          const long long slot = 2 * cluster + (p.first ? 1 : 0);
+          float4* po = A.part_o + slot * 128 * A.rows_pad + r;
+#pragma unroll 1
+          for (int cc = 0; cc < 8; ++cc) {
+            float o[32];
+            tmem_ld32(o_cols + 32 * cc, o);
+            if (!valid) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              po[static_cast<long long>(64 * g + 8 * cc + e) * A.rows_pad] =
+                  make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+          if (g == 0 && valid) A.part_ml[slot * A.rows_pad + r] = make_float2(m, l);
+          if (p.first && threadIdx.x == 128) {
+            const long long at = p.start + kItemCost + x.tiles - 1;
+            int e = static_cast<int>(at * ctl.nc / ctl.total);
+            while (e + 1 < ctl.nc && share_begin(ctl.total, ctl.nc, e + 1) <= at) ++e;
+            while (e > 0 && share_begin(ctl.total, ctl.nc, e) > at) --e;
+            A.rec[cluster] = make_int2(p.item, e);
+            recorded = true;
+          }
+        }
+        ++pieces;
+      }
+      if (threadIdx.x == 128 && !recorded && A.rec) A.rec[cluster] = make_int2(-1, 0);
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();          // the peer no longer touches this CTA's shared memory
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of a cut row tile. CTA (c, y, z): the row tile whose first
+// tile closes cluster c's share, rows 8 y .. 8 y + 7, value dims 128 z on.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) range_join_kernel(const RangeArgs A) {
+  const int c = static_cast<int>(blockIdx.x);
+  const int2 rec = A.rec[c];
+  if (rec.x < 0 || launch_aborted(A.err)) return;
+  const Item x = item_geom(A, rec.x);
+  const int r = 8 * static_cast<int>(blockIdx.y) + static_cast<int>(threadIdx.x & 7);
+  if (r >= x.nrows) return;
+  const int c4 = 32 * static_cast<int>(blockIdx.z) + static_cast<int>(threadIdx.x >> 3);
+  const int n = rec.y - c + 1;                  // parts: slot 1 of c, slot 0 of c+1 .. rec.y
+  auto slot = [&](int i) { return static_cast<long long>(2 * (c + i) + (i == 0 ? 1 : 0)); };
+  float m = -INFINITY;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) m = fmaxf(m, A.part_ml[slot(i) * A.rows_pad + r].x);
+  const float base = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const float2 ml = A.part_ml[slot(i) * A.rows_pad + r];
+    const float4 v = A.part_o[(slot(i) * 128 + c4) * A.rows_pad + r];
+    const float w = fast_exp2(ml.x - base);
+    l += ml.x == -INFINITY ? ml.y : w * ml.y;
+    o.x += w * v.x;
+    o.y += w * v.y;
+    o.z += w * v.z;
+    o.w += w * v.w;
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  __nv_bfloat16* out = A.out + (qr * A.H + h) * 512 + 4 * threadIdx.x;
-  for (int e = 0; e < 4; ++e) out[e] = __float2bfloat16(o[e] * inv);
-  if (threadIdx.x == 0 && A.lse)
-    A.lse[qr * A.H + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+  const __nv_bfloat162 b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  *reinterpret_cast<uint2*>(A.out + (x.row0 + r) * 512 + 4 * c4) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if (c4 == 0 && A.lse)
+    A.lse[x.row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace
 
-cudaError_t launch_range_mla(const RangeArgs& a, cudaStream_t st) {
-  const long long rows = a.block_table ? static_cast<long long>(a.B) * a.nq : a.T;
-  range_mla_kernel<<<static_cast<unsigned>(rows * a.H), kThreads, 0, st>>>(a);
+size_t range_layout(RangeArgs& a, void* workspace) {
+  const int queries = a.block_table ? a.nq : a.T;
+  a.G = std::max(1, std::min(queries, 128 / a.H));
+  a.per_seq = (queries + a.G - 1) / a.G;
+  const long long items = (a.block_table ? static_cast<long long>(a.B) : 1ll) * a.per_seq;
+  a.items = static_cast<int>(items);
+  // tiles a row tile can have
+  const long long keys = a.block_table ? static_cast<long long>(a.max_blocks) * 64 : a.S;
+  long long units = (keys + 63) / 64;
+  if (a.window)
+    units = std::min(units, (static_cast<long long>(a.window) + a.G + 63) / 64 + 1 +
+                                (std::min<long long>(a.sinks, keys) + 63) / 64);
+  const long long tiles = (units + 1) / 2;
+  a.whole = !a.block_table && items > kScanItems;
+  a.clusters = static_cast<int>(std::min<long long>(
+      kMaxClusters, std::max(1ll, items * (tiles + kItemCost) / kMinShare)));
+  a.rows_pad = (a.G * a.H + 7) / 8 * 8;
+  if (a.whole || a.clusters == 1) {
+    a.rec = nullptr;
+    a.part_ml = nullptr;
+    a.part_o = nullptr;
+    return 0;
+  }
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  const size_t n = static_cast<size_t>(a.clusters);
+  const size_t rec = up(n * sizeof(int2)), ml = up(2 * n * a.rows_pad * sizeof(float2));
+  char* ws = static_cast<char*>(workspace);
+  a.rec = reinterpret_cast<int2*>(ws);
+  a.part_ml = ws ? reinterpret_cast<float2*>(ws + rec) : nullptr;
+  a.part_o = ws ? reinterpret_cast<float4*>(ws + rec + ml) : nullptr;
+  return rec + ml + 2 * n * 128 * a.rows_pad * sizeof(float4);
+}
+
+cudaError_t launch_range_mla(const RangeArgs& a_in, cudaStream_t st) {
+  RangeArgs a = a_in;
+  a.kv_rows = a.block_table ? a.nblk * 64 : a.S;
+  const long long q_rows = (a.block_table ? static_cast<long long>(a.B) * a.nq : a.T) * a.H;
+  CUtensorMap tq, tk, tv;
+  cudaError_t e = make_tmap_2d(&tq, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 576, q_rows, 576 * 2,
+                               64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (e == cudaSuccess) e = make_tmap_chunks(&tk, a.kv, a.kv_rows, 64, 1);
+  if (e == cudaSuccess) e = make_tmap_chunks(&tv, a.kv, a.kv_rows, 64, 4);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(range_mla_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kSmemBytes));
+  if (e != cudaSuccess) return e;
+  range_mla_kernel<<<2 * a.clusters, kThreads, kSmemBytes, st>>>(tq, tk, tv, a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || !a.rec) return e;
+  range_join_kernel<<<dim3(a.clusters, a.rows_pad / 8, 4), kJoinThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
