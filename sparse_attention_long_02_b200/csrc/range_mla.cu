@@ -16,9 +16,10 @@
 // Two roles in a cluster of two CTAs. A 128 x 512 fp32 output fills the 512
 // TMEM columns of an SM, so one SM cannot hold it beside the logits. CTA 0
 // forms the logits and the softmax, CTA 1 the output:
-//   CTA 0: K chunks (128 keys x 64 dims) stream through a ring of TMA loads;
-//     S = Q K^T (M = 128, N = 128, K = 576) goes into one of four TMEM
-//     buffers; two groups of four warps (thread = row) take the tiles in
+//   CTA 0: Q's 512 latent dims move into TMEM (256 columns; the rope dims stay
+//     in shared memory), K chunks (128 keys x 64 dims) stream through a ring of
+//     TMA loads; S = Q K^T (M = 128, N = 128, K = 576) goes into one of two
+//     TMEM buffers; two groups of four warps (thread = row) take the tiles in
 //     turn: row maximum, running reference maximum (re-based only when it
 //     grows by more than 8 in log2 units), P = exp2(z - m) in bf16 into shared
 //     memory, one 16 KB bulk copy per 64 keys into CTA 1.
@@ -43,14 +44,17 @@
 namespace dsa {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kQAtom = 128 * 128;               // 128 rows x 64 dims bf16, 128-B swizzled
 constexpr int kChunk = 128 * 128;               // 128 keys x 64 dims
 constexpr int kUnitChunk = 64 * 128;            // 64 keys x 64 dims
 constexpr int kPAtom = 128 * 128;               // P: 128 rows x 64 keys
 constexpr int kVChunk = 4 * kUnitChunk;         // 64 keys x 256 dims
-constexpr int kKRing = 3;
-constexpr int kSBufs = 4;
+// Even, so that each of the two loading warps has its own places and sees every
+// phase of their barriers.
+constexpr int kRing = 10;
+constexpr int kQTmemAtoms = 8;                  // Q dims [0, 512) live in TMEM
+constexpr uint32_t kColQ = 256;                 // after two buffers of 128 logits
 constexpr int kPSlots = 4;
 constexpr int kVRing = 4;
 constexpr int kAhead = 3;                       // tiles of L2 prefetch
@@ -61,8 +65,8 @@ constexpr int kItemCost = 1;                    // a row tile's fixed cost, in t
 constexpr int kMinShare = 2;                    // tiles (and fixed costs) a cluster takes at least
 
 struct LogitsSmem {                             // CTA 0
-  uint8_t q[9][kQAtom];
-  uint8_t k[kKRing][kChunk];
+  uint8_t ring[kRing][kChunk];                  // chunks of K, and of Q on its way to TMEM
+  uint8_t q_rope[2][kQAtom];                    // Q dims [512, 576), by piece parity
   uint8_t p[2][kPAtom];                         // each softmax group's staging of P
 };
 struct OutputSmem {                             // CTA 1
@@ -78,9 +82,11 @@ struct Ctl {
   float m[2][128];                              // CTA 0: reference maxima, by tile parity
   unsigned flag[4][4];                          // CTA 1: [tile][lane quarter] rescale wanted
   // CTA 0
-  unsigned long long q_full, q_free;
-  unsigned long long k_full[kKRing], k_empty[kKRing];
-  unsigned long long s_full[kSBufs], s_empty[kSBufs];
+  unsigned long long q_free;                    // the piece's last QK is done
+  unsigned long long q_ready[kQTmemAtoms];      // a chunk of Q is in TMEM
+  unsigned long long rope_full[2], rope_free[2];
+  unsigned long long k_full[kRing], k_empty[kRing];
+  unsigned long long s_full[2], s_empty[2];     // by softmax group
   unsigned long long m_bar[4];                  // a tile's reference maxima of a lane quarter
   // by softmax group, so that whoever waits on one sees every phase of it
   unsigned long long p_own[2];                  // a staged atom is written
@@ -318,15 +324,13 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   find_share(A, ctl, reinterpret_cast<long long*>(big), cluster);
   if (threadIdx.x == 0) {
     auto init = [](unsigned long long& b, int count) { mbar_init(smem_u32(&b), count); };
-    init(ctl.q_full, 1);
     init(ctl.q_free, 1);
-    for (int i = 0; i < kKRing; ++i) {
+    for (int i = 0; i < kQTmemAtoms; ++i) init(ctl.q_ready[i], 4);
+    for (int i = 0; i < kRing; ++i) {
       init(ctl.k_full[i], 1);
       init(ctl.k_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
-      init(ctl.s_full[i], 1);
-      init(ctl.s_empty[i], 4);
       init(ctl.m_bar[i], 1);
       init(ctl.p_room[i], 1);
       init(ctl.v_full[i], 1);
@@ -338,6 +342,10 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       init(ctl.pv_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      init(ctl.rope_full[i], 1);
+      init(ctl.rope_free[i], 1);
+      init(ctl.s_full[i], 1);
+      init(ctl.s_empty[i], 4);
       init(ctl.p_own[i], 4);
       init(ctl.p_ack[i], 1);
     }
@@ -369,21 +377,13 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (rank == 0) {
     if (warp == 0 || warp == 2) {
       // ------------------------------------------------ Q and K loads (CTA 0)
-      // Two warps take the K chunks in turn: a wait, an expect and a load cost
-      // one thread about 360 cycles, a chunk's MMAs only 274.
+      // Two warps take the ring's entries in turn: a wait, an expect and a load
+      // cost one thread about 360 cycles, a chunk's MMAs only 274. In a piece's
+      // first tile each K chunk follows the Q chunk it is multiplied with.
       const int par = warp >> 1;
       if (lane == 0) {
-        int kc = 0, pieces = 0;
-        const uint32_t qf = smem_u32(&ctl.q_full);
+        int ent = 0, pieces = 0;
         while (ok && walk.next(A, p, x)) {
-          if (par == 0) {
-            if (pieces > 0 &&
-                !(ok = mbar_wait(smem_u32(&ctl.q_free), (pieces - 1) & 1, abort_flag, err)))
-              break;
-            mbar_expect_tx(qf, 9 * kQAtom);
-            for (int a = 0; a < 9; ++a)
-              tma_load_2d(smem_u32(sl.q[a]), &tm_q, qf, 64 * a, static_cast<int>(x.row0));
-          }
           auto prefetch_tile = [&](int t) {
             if (t >= p.t1) return;
             for (int u = 2 * t; u < min(2 * t + 2, x.nu); ++u) {
@@ -393,8 +393,17 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             1152u * static_cast<unsigned>(min(64, A.kv_rows - row)));
             }
           };
-          if (par == 0)
+          if (par == 0) {
+            // the rope chunk of two pieces ago was read by its last QK
+            if (pieces > 1 && !(ok = mbar_wait(smem_u32(&ctl.rope_free[pieces & 1]),
+                                               ((pieces >> 1) + 1) & 1, abort_flag, err)))
+              break;
+            const uint32_t full = smem_u32(&ctl.rope_full[pieces & 1]);
+            mbar_expect_tx(full, kQAtom);
+            tma_load_2d(smem_u32(sl.q_rope[pieces & 1]), &tm_q, full, 64 * kQTmemAtoms,
+                        static_cast<int>(x.row0));
             for (int t = 1; t < kAhead; ++t) prefetch_tile(p.t0 + t);
+          }
           int r0 = unit_row(A, x, 2 * p.t0), r1 = unit_row(A, x, 2 * p.t0 + 1);
           for (int t = p.t0; ok && t < p.t1; ++t) {
             const int n = tile_units(x, t);
@@ -402,58 +411,125 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             r0 = unit_row(A, x, 2 * t + 2);
             r1 = unit_row(A, x, 2 * t + 3);
             if (par == 0) prefetch_tile(t + kAhead);
-            for (int ch = 0; ch < 9; ++ch, ++kc) {
-              if ((kc & 1) != par) continue;
-              const int st = kc % kKRing;
-              if (kc >= kKRing && !(ok = mbar_wait(smem_u32(&ctl.k_empty[st]),
-                                                   (kc / kKRing + 1) & 1, abort_flag, err)))
+            const bool with_q = t == p.t0;
+            for (int i = 0; i < (with_q ? 9 + kQTmemAtoms : 9); ++i, ++ent) {
+              if ((ent & 1) != par) continue;
+              const int st = ent % kRing;
+              if (ent >= kRing && !(ok = mbar_wait(smem_u32(&ctl.k_empty[st]),
+                                                   (ent / kRing + 1) & 1, abort_flag, err)))
                 break;
               const uint32_t full = smem_u32(&ctl.k_full[st]);
-              mbar_expect_tx(full, n * kUnitChunk);
-              tma_load_3d(smem_u32(sl.k[st]), &tm_k, full, 0, c0, ch);
-              if (n > 1) tma_load_3d(smem_u32(sl.k[st] + kUnitChunk), &tm_k, full, 0, c1, ch);
+              const int ch = with_q ? i >> 1 : i;
+              if (with_q && !(i & 1) && ch < kQTmemAtoms) {
+                mbar_expect_tx(full, kQAtom);
+                tma_load_2d(smem_u32(sl.ring[st]), &tm_q, full, 64 * ch,
+                            static_cast<int>(x.row0));
+              } else {
+                mbar_expect_tx(full, n * kUnitChunk);
+                tma_load_3d(smem_u32(sl.ring[st]), &tm_k, full, 0, c0, ch);
+                if (n > 1) tma_load_3d(smem_u32(sl.ring[st] + kUnitChunk), &tm_k, full, 0, c1, ch);
+              }
             }
           }
           ++pieces;
         }
         if (!ok) {           // let the loads in flight land before this CTA leaves
-          for (int c = max(0, kc - kKRing); c < kc; ++c)
-            if ((c & 1) == par) mbar_drain(smem_u32(&ctl.k_full[c % kKRing]), (c / kKRing) & 1);
-          if (par == 0 && pieces >= 0) mbar_drain(qf, pieces & 1);
+          for (int c = max(0, ent - kRing); c < ent; ++c)
+            if ((c & 1) == par) mbar_drain(smem_u32(&ctl.k_full[c % kRing]), (c / kRing) & 1);
+          if (par == 0)
+            for (int c = 0; c < 2; ++c)
+              if (pieces >= c) mbar_drain(smem_u32(&ctl.rope_full[(pieces - c) & 1]),
+                                          ((pieces - c) >> 1) & 1);
         }
+      }
+    } else if (warp >= 12) {
+      // ------------------------------------------- Q into TMEM (CTA 0)
+      // Row r of each chunk, bf16 pairs, lane = row; once the piece before no
+      // longer reads Q. (That wait also means every entry of that piece has
+      // been consumed, so the barriers waited on below are in the phase before.)
+      const int r = 32 * (warp & 3) + lane;
+      const uint32_t q_cols = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kColQ;
+      int ent = 0, pieces = 0;
+      while (ok && walk.next(A, p, x)) {
+        if (pieces > 0 &&
+            !(ok = warp_wait(smem_u32(&ctl.q_free), (pieces - 1) & 1, abort_flag, err)))
+          break;
+        tc_fence_after();
+        for (int ch = 0; ch < kQTmemAtoms; ++ch) {
+          const int e = ent + 2 * ch, st = e % kRing;
+          if (!(ok = warp_wait(smem_u32(&ctl.k_full[st]), (e / kRing) & 1, abort_flag, err))) break;
+          const uint4* row = reinterpret_cast<const uint4*>(sl.ring[st] + r * 128);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const uint4 v = row[(4 * half + c) ^ (r & 7)];
+              pk[4 * c] = v.x;
+              pk[4 * c + 1] = v.y;
+              pk[4 * c + 2] = v.z;
+              pk[4 * c + 3] = v.w;
+            }
+            tmem_st16(q_cols + 32 * ch + 16 * half, pk);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.q_ready[ch]));
+        }
+        ent += 9 * (p.t1 - p.t0) + kQTmemAtoms;
+        ++pieces;
       }
     } else if (warp == 1) {
       // ------------------------------------------------------- QK (CTA 0)
       const uint32_t id2 = idesc_bf16(128, 128, false), id1 = idesc_bf16(128, 64, false);
-      int kc = 0, tc = 0, pieces = 0;
+      int ent = 0, tc = 0, pieces = 0;
       // debug: ml_free completes only after an output is written, so this
       // bounded wait runs out and both CTAs leave through their give-up paths
       if (ok && (debug_bits(err) & kDbgStallMla))
         ok = warp_wait(smem_u32(&ctl.ml_free), 0, abort_flag, err);
       while (ok && walk.next(A, p, x)) {
-        if (!(ok = warp_wait(smem_u32(&ctl.q_full), pieces & 1, abort_flag, err))) break;
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
-          const int sb = tc & 3;
-          if (tc >= kSBufs &&
-              !(ok = warp_wait(smem_u32(&ctl.s_empty[sb]), ((tc >> 2) + 1) & 1, abort_flag, err)))
+          const int sb = tc & 1;
+          if (tc >= 2 &&
+              !(ok = warp_wait(smem_u32(&ctl.s_empty[sb]), ((tc >> 1) + 1) & 1, abort_flag, err)))
             break;
           tc_fence_after();
           const uint32_t d = tmem + 128 * sb;
           const uint32_t id = tile_units(x, t) > 1 ? id2 : id1;
-          for (int ch = 0; ch < 9; ++ch, ++kc) {
-            const int st = kc % kKRing;
-            if (!(ok = warp_wait(smem_u32(&ctl.k_full[st]), (kc / kKRing) & 1, abort_flag, err)))
+          for (int ch = 0; ch < 9; ++ch, ++ent) {
+            if (t == p.t0 && ch < kQTmemAtoms) {
+              // Q's chunk has left its place in the ring
+              if (!(ok = warp_wait(smem_u32(&ctl.q_ready[ch]), pieces & 1, abort_flag, err))) break;
+              if (lane == 0) mbar_arrive(smem_u32(&ctl.k_empty[ent % kRing]));
+              ++ent;
+              tc_fence_after();
+            } else if (t == p.t0) {
+              if (!(ok = warp_wait(smem_u32(&ctl.rope_full[pieces & 1]), (pieces >> 1) & 1,
+                                   abort_flag, err)))
+                break;
+            }
+            const int st = ent % kRing;
+            if (!(ok = warp_wait(smem_u32(&ctl.k_full[st]), (ent / kRing) & 1, abort_flag, err)))
               break;
             if (elect_one()) {
-              const uint64_t qd = sdesc_sw128(smem_u32(sl.q[ch]), 0, 1024);
-              const uint64_t kd = sdesc_sw128(smem_u32(sl.k[st]), 0, 1024);
+              const uint64_t kd = sdesc_sw128(smem_u32(sl.ring[st]), 0, 1024);
+              if (ch < kQTmemAtoms) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16(d, qd + 2 * kk, kd + 2 * kk, id, (ch > 0 || kk > 0) ? 1u : 0u);
+                for (int kk = 0; kk < 4; ++kk)          // 16 dims: 8 TMEM columns of Q
+                  mma_bf16_ts(d, tmem + kColQ + 32 * ch + 8 * kk, kd + 2 * kk, id,
+                              (ch > 0 || kk > 0) ? 1u : 0u);
+              } else {
+                const uint64_t qd = sdesc_sw128(smem_u32(sl.q_rope[pieces & 1]), 0, 1024);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) mma_bf16(d, qd + 2 * kk, kd + 2 * kk, id, 1u);
+              }
               mma_commit(smem_u32(&ctl.k_empty[st]));
               if (ch == 8) {
                 mma_commit(smem_u32(&ctl.s_full[sb]));
-                if (t + 1 == p.t1) mma_commit(smem_u32(&ctl.q_free));
+                if (t + 1 == p.t1) {
+                  mma_commit(smem_u32(&ctl.q_free));
+                  mma_commit(smem_u32(&ctl.rope_free[pieces & 1]));
+                }
               }
             }
             __syncwarp();
@@ -510,7 +586,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int t = p.t0; ok && t < p.t1; ++t) {
           const int n = tile_units(x, t);
           if ((tc & 1) == g) {
-            const int sb = tc & 3;
             unsigned long long vis[2] = {0ull, 0ull};
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
@@ -526,23 +601,28 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               const int kb = block * 64;
               if (good) vis[u] = range_bits(lo - kb, hi - kb) | range_bits(0, sink_hi - kb);
             }
-            if (!(ok = warp_wait(smem_u32(&ctl.s_full[sb]), (tc >> 2) & 1, abort_flag, err))) break;
+            if (!(ok = warp_wait(smem_u32(&ctl.s_full[g]), (tc >> 1) & 1, abort_flag, err))) break;
             tc_fence_after();
-            const uint32_t s_cols = tmem + lanes + 128 * sb;
+            const uint32_t s_cols = tmem + lanes + 128 * g;
             float mx = -INFINITY;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               if (u >= n) continue;
               float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-              float s[64];
-              tmem_ld64(s_cols + 64 * u, s);
-              if (__all_sync(0xffffffffu, vis[u] == ~0ull)) {
+              const bool all = __all_sync(0xffffffffu, vis[u] == ~0ull);
 #pragma unroll
-                for (int e = 0; e < 64; ++e) pm[e & 3] = fmaxf(pm[e & 3], s[e]);
-              } else {
+              for (int h = 0; h < 2; ++h) {
+                float s[32];
+                tmem_ld32(s_cols + 64 * u + 32 * h, s);
+                if (all) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                  pm[e & 3] = fmaxf(pm[e & 3], (vis[u] >> e) & 1ull ? s[e] : -INFINITY);
+                  for (int e = 0; e < 32; ++e) pm[e & 3] = fmaxf(pm[e & 3], s[e]);
+                } else {
+                  const unsigned bits = static_cast<unsigned>(vis[u] >> (32 * h));
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    pm[e & 3] = fmaxf(pm[e & 3], (bits >> e) & 1u ? s[e] : -INFINITY);
+                }
               }
               mx = fmaxf(mx, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));
             }
@@ -565,28 +645,34 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               if (u >= n) continue;
-              float s[64];
-              tmem_ld64(s_cols + 64 * u, s);
-              if (u + 1 == n) {                         // the buffer is free for another tile
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl.s_empty[sb]));
-              }
               float ps[4] = {0.f, 0.f, 0.f, 0.f};
               uint32_t pk[32];
-              if (__all_sync(0xffffffffu, vis[u] == ~0ull)) {
+              const bool all = __all_sync(0xffffffffu, vis[u] == ~0ull);
 #pragma unroll
-                for (int e = 0; e < 64; ++e) s[e] = fast_exp2(fmaf(s[e], A.sm_scale_log2, -base));
-              } else {
+              for (int h = 0; h < 2; ++h) {
+                float s[32];
+                tmem_ld32(s_cols + 64 * u + 32 * h, s);
+                if (h == 1 && u + 1 == n) {             // the buffer is free for another tile
+                  tc_fence_before();
+                  __syncwarp();
+                  if (lane == 0) mbar_arrive(smem_u32(&ctl.s_empty[g]));
+                }
+                if (all) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                  s[e] = (vis[u] >> e) & 1ull ? fast_exp2(fmaf(s[e], A.sm_scale_log2, -base)) : 0.f;
-              }
+                  for (int e = 0; e < 32; ++e)
+                    s[e] = fast_exp2(fmaf(s[e], A.sm_scale_log2, -base));
+                } else {
+                  const unsigned bits = static_cast<unsigned>(vis[u] >> (32 * h));
 #pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                ps[e & 3] += s[2 * e] + s[2 * e + 1];
-                const __nv_bfloat162 pb = __floats2bfloat162_rn(s[2 * e], s[2 * e + 1]);
-                pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
+                  for (int e = 0; e < 32; ++e)
+                    s[e] = (bits >> e) & 1u ? fast_exp2(fmaf(s[e], A.sm_scale_log2, -base)) : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  ps[e & 3] += s[2 * e] + s[2 * e + 1];
+                  const __nv_bfloat162 pb = __floats2bfloat162_rn(s[2 * e], s[2 * e + 1]);
+                  pk[16 * h + e] = *reinterpret_cast<const uint32_t*>(&pb);
+                }
               }
               l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
               if (atoms > 0 && !(ok = warp_wait<true>(smem_u32(&ctl.p_ack[g]), (atoms - 1) & 1,
@@ -703,8 +789,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       if (!ok) {
         if (elect_one()) {
-          mma_commit(smem_u32(&ctl.q_full));
-          mbar_drain(smem_u32(&ctl.q_full), 0);
+          mma_commit(smem_u32(&ctl.q_free));
+          mbar_drain(smem_u32(&ctl.q_free), 0);
         }
         __syncwarp();
       }
@@ -731,7 +817,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
       }
-    } else {
+    } else if (warp < 12) {
       // ------------------------------------- rescale and output (CTA 1)
       const int g = (warp - 4) >> 2;                    // half of the 512 value dims
       const int wq = warp & 3;
