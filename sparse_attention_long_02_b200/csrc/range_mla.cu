@@ -45,15 +45,14 @@ namespace dsa {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kQAtom = 128 * 128;               // 128 rows x 64 dims bf16, 128-B swizzled
-constexpr int kChunk = 128 * 128;               // 128 keys x 64 dims
-constexpr int kUnitChunk = 64 * 128;            // 64 keys x 64 dims
-constexpr int kPAtom = 128 * 128;               // P: 128 rows x 64 keys
-constexpr int kVChunk = 4 * kUnitChunk;         // 64 keys x 256 dims
+constexpr int kAtom = 128 * 128;                // 128 rows (or keys) x 64 dims, 128-B swizzled
+constexpr int kUnitAtom = 64 * 128;             // 64 keys x 64 dims
+constexpr int kEntry = 2 * kAtom;               // ring entry: 128 dims of 128 rows
+constexpr int kVChunk = 4 * kUnitAtom;          // 64 keys x 256 dims
 // Even, so that each of the two loading warps has its own places and sees every
 // phase of their barriers.
-constexpr int kRing = 10;
-constexpr int kQTmemAtoms = 8;                  // Q dims [0, 512) live in TMEM
+constexpr int kRing = 4;
+constexpr int kQPairs = 4;                      // Q dims [0, 512) live in TMEM, 128 at a time
 constexpr uint32_t kColQ = 256;                 // after two buffers of 128 logits
 constexpr int kPSlots = 4;
 constexpr int kVRing = 4;
@@ -65,12 +64,14 @@ constexpr int kItemCost = 1;                    // a row tile's fixed cost, in t
 constexpr int kMinShare = 2;                    // tiles (and fixed costs) a cluster takes at least
 
 struct LogitsSmem {                             // CTA 0
-  uint8_t ring[kRing][kChunk];                  // chunks of K, and of Q on its way to TMEM
-  uint8_t q_rope[2][kQAtom];                    // Q dims [512, 576), by piece parity
-  uint8_t p[2][kPAtom];                         // each softmax group's staging of P
+  uint8_t ring[kRing][kEntry];                  // K, and Q on its way to TMEM
+  uint8_t p[2][2][kAtom];                       // staging of P, by softmax group and unit
+  uint8_t q_rope[kAtom];                        // Q dims [512, 576)
+  float alpha[2][128];                          // staging of the rescale factors, by group
+  float m[2][128];                              // reference maxima, by tile parity
 };
 struct OutputSmem {                             // CTA 1
-  uint8_t p[kPSlots][kPAtom];
+  uint8_t p[kPSlots][kAtom];
   uint8_t v[kVRing][kVChunk];
   float alpha[4][128];                          // rescale factors, by tile
   float2 ml[2][128];                            // maximum and sum of each softmax group
@@ -79,18 +80,16 @@ constexpr size_t kBig = sizeof(LogitsSmem);
 static_assert(sizeof(OutputSmem) <= kBig && kBig % 1024 == 0, "both roles fit");
 
 struct Ctl {
-  float m[2][128];                              // CTA 0: reference maxima, by tile parity
-  unsigned flag[4][4];                          // CTA 1: [tile][lane quarter] rescale wanted
   // CTA 0
   unsigned long long q_free;                    // the piece's last QK is done
-  unsigned long long q_ready[kQTmemAtoms];      // a chunk of Q is in TMEM
-  unsigned long long rope_full[2], rope_free[2];
+  unsigned long long q_ready[kQPairs];          // 128 dims of Q are in TMEM
+  unsigned long long rope_full;
   unsigned long long k_full[kRing], k_empty[kRing];
   unsigned long long s_full[2], s_empty[2];     // by softmax group
   unsigned long long m_bar[4];                  // a tile's reference maxima of a lane quarter
-  // by softmax group, so that whoever waits on one sees every phase of it
-  unsigned long long p_own[2];                  // a staged atom is written
-  unsigned long long p_ack[2];                  // CTA 1 holds the atom: its staging is free
+  // by softmax group and unit, so that whoever waits on one sees every phase
+  unsigned long long p_own[2][2];               // a staged atom is written
+  unsigned long long p_ack[2][2];               // CTA 1 holds the atom: its staging is free
   unsigned long long p_room[kPSlots];           // CTA 1 has room for another atom
   unsigned long long ml_free;                   // CTA 1 has read ml
   // CTA 1
@@ -193,7 +192,8 @@ struct Walk {
   long long start;
   __device__ __forceinline__ Walk(const Ctl& c)
       : item(c.item), off(c.off), left(c.left), start(c.start) {}
-  __device__ __forceinline__ bool next(const RangeArgs& A, Piece& p, Item& x) {
+  // Out of line: every role calls it, once a piece.
+  __device__ __noinline__ bool step(const RangeArgs& A, Piece& p, Item& x) {
     if (A.whole) {
       // later rows of a prefill see more keys: they go first
       if (item >= A.items) return false;
@@ -223,7 +223,37 @@ struct Walk {
     }
     return false;
   }
+  // (through copies, so that the caller's stay in registers)
+  __device__ __forceinline__ bool next(const RangeArgs& A, Piece& p, Item& x) {
+    Piece p1;
+    Item x1;
+    const bool more = step(A, p1, x1);
+    p = p1;
+    x = x1;
+    return more;
+  }
 };
+
+// The bounded waits of common.cuh with the slow path out of line: this kernel
+// has some thirty of them in sixteen warps that run different code, and short
+// loops that have to fit the instruction caches.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                       unsigned* err) {
+  return mbar_wait<true>(bar, parity, abort_flag, err);
+}
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait1(unsigned long long& b, uint32_t parity,
+                                      volatile int* abort_flag, unsigned* err) {
+  const uint32_t bar = smem_u32(&b);
+  if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+  return wait_slow(bar, parity, abort_flag, err);
+}
+// By every lane of a warp, which agrees on the result.
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait32(unsigned long long& b, uint32_t parity,
+                                       volatile int* abort_flag, unsigned* err) {
+  return __all_sync(0xffffffffu, wait1<kCluster>(b, parity, abort_flag, err));
+}
 
 __device__ __forceinline__ long long share_begin(long long total, int nc, int c) {
   return total * c / nc;
@@ -309,7 +339,8 @@ __device__ __forceinline__ unsigned long long range_bits(int a, int b) {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                 const __grid_constant__ CUtensorMap tm_v, const RangeArgs A) {
+                 const __grid_constant__ CUtensorMap tm_v,
+                 const __grid_constant__ RangeArgs A) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* big = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                             ~static_cast<uintptr_t>(1023));
@@ -325,29 +356,26 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (threadIdx.x == 0) {
     auto init = [](unsigned long long& b, int count) { mbar_init(smem_u32(&b), count); };
     init(ctl.q_free, 1);
-    for (int i = 0; i < kQTmemAtoms; ++i) init(ctl.q_ready[i], 4);
-    for (int i = 0; i < kRing; ++i) {
+    init(ctl.rope_full, 1);
+    for (int i = 0; i < 4; ++i) {
+      init(ctl.q_ready[i], 4);
       init(ctl.k_full[i], 1);
       init(ctl.k_empty[i], 1);
-    }
-    for (int i = 0; i < 4; ++i) {
       init(ctl.m_bar[i], 1);
+      init(ctl.p_own[i >> 1][i & 1], 4);
+      init(ctl.p_ack[i >> 1][i & 1], 1);
       init(ctl.p_room[i], 1);
       init(ctl.v_full[i], 1);
       init(ctl.v_empty[i], 1);
       init(ctl.p_full[i], 1);
       init(ctl.p_free[i], 1);
-      init(ctl.al_full[i], 4);
+      init(ctl.al_full[i], 1);
       init(ctl.o_ok[i], 8);
       init(ctl.pv_done[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      init(ctl.rope_full[i], 1);
-      init(ctl.rope_free[i], 1);
       init(ctl.s_full[i], 1);
       init(ctl.s_empty[i], 4);
-      init(ctl.p_own[i], 4);
-      init(ctl.p_ack[i], 1);
     }
     init(ctl.ml_free, 8);
     init(ctl.o_done, 1);
@@ -356,7 +384,10 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     fence_barrier_init();
     // CTA 1 expects the first atoms of P before CTA 0 can send one
     if (rank == 1)
-      for (int i = 0; i < kPSlots; ++i) mbar_expect_tx(smem_u32(&ctl.p_full[i]), kPAtom);
+      for (int i = 0; i < 4; ++i) {
+        mbar_expect_tx(smem_u32(&ctl.p_full[i]), kAtom);
+        mbar_expect_tx(smem_u32(&ctl.al_full[i]), 512);
+      }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&ctl.tmem_base), 512);
@@ -377,9 +408,9 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (rank == 0) {
     if (warp == 0 || warp == 2) {
       // ------------------------------------------------ Q and K loads (CTA 0)
-      // Two warps take the ring's entries in turn: a wait, an expect and a load
-      // cost one thread about 360 cycles, a chunk's MMAs only 274. In a piece's
-      // first tile each K chunk follows the Q chunk it is multiplied with.
+      // Two warps take the ring's entries in turn: a wait, an expect and four
+      // loads cost one thread about 540 cycles, an entry's MMAs 549. In a
+      // piece's first tile each K entry follows the Q entry it meets.
       const int par = warp >> 1;
       if (lane == 0) {
         int ent = 0, pieces = 0;
@@ -393,17 +424,9 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             1152u * static_cast<unsigned>(min(64, A.kv_rows - row)));
             }
           };
-          if (par == 0) {
-            // the rope chunk of two pieces ago was read by its last QK
-            if (pieces > 1 && !(ok = mbar_wait(smem_u32(&ctl.rope_free[pieces & 1]),
-                                               ((pieces >> 1) + 1) & 1, abort_flag, err)))
-              break;
-            const uint32_t full = smem_u32(&ctl.rope_full[pieces & 1]);
-            mbar_expect_tx(full, kQAtom);
-            tma_load_2d(smem_u32(sl.q_rope[pieces & 1]), &tm_q, full, 64 * kQTmemAtoms,
-                        static_cast<int>(x.row0));
+          if (par == 0)
             for (int t = 1; t < kAhead; ++t) prefetch_tile(p.t0 + t);
-          }
+          const int q_row = static_cast<int>(x.row0);
           int r0 = unit_row(A, x, 2 * p.t0), r1 = unit_row(A, x, 2 * p.t0 + 1);
           for (int t = p.t0; ok && t < p.t1; ++t) {
             const int n = tile_units(x, t);
@@ -412,22 +435,36 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             r1 = unit_row(A, x, 2 * t + 3);
             if (par == 0) prefetch_tile(t + kAhead);
             const bool with_q = t == p.t0;
-            for (int i = 0; i < (with_q ? 9 + kQTmemAtoms : 9); ++i, ++ent) {
+            const int count = with_q ? 5 + kQPairs : 5;
+#pragma unroll 1
+            for (int i = 0; i < count; ++i, ++ent) {
+              const bool last = i + 1 == count;
+              if (with_q && last && par == 0) {
+                // the rope dims of Q, once the piece before no longer reads its own
+                if (pieces > 0 && !(ok = wait1(ctl.q_free, (pieces - 1) & 1, abort_flag, err)))
+                  break;
+                mbar_expect_tx(smem_u32(&ctl.rope_full), kAtom);
+                tma_load_2d(smem_u32(sl.q_rope), &tm_q, smem_u32(&ctl.rope_full), 512, q_row);
+              }
               if ((ent & 1) != par) continue;
-              const int st = ent % kRing;
-              if (ent >= kRing && !(ok = mbar_wait(smem_u32(&ctl.k_empty[st]),
-                                                   (ent / kRing + 1) & 1, abort_flag, err)))
+              const int st = ent & (kRing - 1);
+              if (ent >= kRing &&
+                  !(ok = wait1(ctl.k_empty[st], (ent / kRing + 1) & 1, abort_flag, err)))
                 break;
-              const uint32_t full = smem_u32(&ctl.k_full[st]);
-              const int ch = with_q ? i >> 1 : i;
-              if (with_q && !(i & 1) && ch < kQTmemAtoms) {
-                mbar_expect_tx(full, kQAtom);
-                tma_load_2d(smem_u32(sl.ring[st]), &tm_q, full, 64 * ch,
-                            static_cast<int>(x.row0));
+              const uint32_t full = smem_u32(&ctl.k_full[st]), dst = smem_u32(sl.ring[st]);
+              const int ch = 2 * (with_q ? i >> 1 : i);           // first 64-dim chunk
+              if (with_q && !last && !(i & 1)) {
+                mbar_expect_tx(full, kEntry);
+                tma_load_2d(dst, &tm_q, full, 64 * ch, q_row);
+                tma_load_2d(dst + kAtom, &tm_q, full, 64 * ch + 64, q_row);
               } else {
-                mbar_expect_tx(full, n * kUnitChunk);
-                tma_load_3d(smem_u32(sl.ring[st]), &tm_k, full, 0, c0, ch);
-                if (n > 1) tma_load_3d(smem_u32(sl.ring[st] + kUnitChunk), &tm_k, full, 0, c1, ch);
+                mbar_expect_tx(full, (last ? 1 : 2) * n * kUnitAtom);
+                tma_load_3d(dst, &tm_k, full, 0, c0, ch);
+                if (n > 1) tma_load_3d(dst + kUnitAtom, &tm_k, full, 0, c1, ch);
+                if (!last) {
+                  tma_load_3d(dst + kAtom, &tm_k, full, 0, c0, ch + 1);
+                  if (n > 1) tma_load_3d(dst + kAtom + kUnitAtom, &tm_k, full, 0, c1, ch + 1);
+                }
               }
             }
           }
@@ -435,105 +472,101 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (!ok) {           // let the loads in flight land before this CTA leaves
           for (int c = max(0, ent - kRing); c < ent; ++c)
-            if ((c & 1) == par) mbar_drain(smem_u32(&ctl.k_full[c % kRing]), (c / kRing) & 1);
-          if (par == 0)
-            for (int c = 0; c < 2; ++c)
-              if (pieces >= c) mbar_drain(smem_u32(&ctl.rope_full[(pieces - c) & 1]),
-                                          ((pieces - c) >> 1) & 1);
+            if ((c & 1) == par)
+              mbar_drain(smem_u32(&ctl.k_full[c & (kRing - 1)]), (c / kRing) & 1);
+          if (par == 0) mbar_drain(smem_u32(&ctl.rope_full), pieces & 1);
         }
       }
     } else if (warp >= 12) {
       // ------------------------------------------- Q into TMEM (CTA 0)
-      // Row r of each chunk, bf16 pairs, lane = row; once the piece before no
+      // Row r of each entry, bf16 pairs, lane = row; once the piece before no
       // longer reads Q. (That wait also means every entry of that piece has
       // been consumed, so the barriers waited on below are in the phase before.)
       const int r = 32 * (warp & 3) + lane;
       const uint32_t q_cols = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kColQ;
       int ent = 0, pieces = 0;
       while (ok && walk.next(A, p, x)) {
-        if (pieces > 0 &&
-            !(ok = warp_wait(smem_u32(&ctl.q_free), (pieces - 1) & 1, abort_flag, err)))
-          break;
+        if (pieces > 0 && !(ok = wait32(ctl.q_free, (pieces - 1) & 1, abort_flag, err))) break;
         tc_fence_after();
-        for (int ch = 0; ch < kQTmemAtoms; ++ch) {
-          const int e = ent + 2 * ch, st = e % kRing;
-          if (!(ok = warp_wait(smem_u32(&ctl.k_full[st]), (e / kRing) & 1, abort_flag, err))) break;
-          const uint4* row = reinterpret_cast<const uint4*>(sl.ring[st] + r * 128);
+#pragma unroll 1
+        for (int j = 0; j < kQPairs; ++j) {
+          const int e = ent + 2 * j, st = e & (kRing - 1);
+          if (!(ok = wait32(ctl.k_full[st], (e / kRing) & 1, abort_flag, err))) break;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
+          for (int half = 0; half < 4; ++half) {
+            const uint4* row =
+                reinterpret_cast<const uint4*>(sl.ring[st] + (half >> 1) * kAtom + r * 128);
             uint32_t pk[16];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              const uint4 v = row[(4 * half + c) ^ (r & 7)];
+              const uint4 v = row[(4 * (half & 1) + c) ^ (r & 7)];
               pk[4 * c] = v.x;
               pk[4 * c + 1] = v.y;
               pk[4 * c + 2] = v.z;
               pk[4 * c + 3] = v.w;
             }
-            tmem_st16(q_cols + 32 * ch + 16 * half, pk);
+            tmem_st16(q_cols + 64 * j + 16 * half, pk);
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl.q_ready[ch]));
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.q_ready[j]));
         }
-        ent += 9 * (p.t1 - p.t0) + kQTmemAtoms;
+        ent += 5 * (p.t1 - p.t0) + kQPairs;
         ++pieces;
       }
     } else if (warp == 1) {
       // ------------------------------------------------------- QK (CTA 0)
       const uint32_t id2 = idesc_bf16(128, 128, false), id1 = idesc_bf16(128, 64, false);
+      const uint64_t ring_d = sdesc_sw128(smem_u32(sl.ring[0]), 0, 1024);
+      const uint64_t rope_d = sdesc_sw128(smem_u32(sl.q_rope), 0, 1024);
       int ent = 0, tc = 0, pieces = 0;
       // debug: ml_free completes only after an output is written, so this
       // bounded wait runs out and both CTAs leave through their give-up paths
-      if (ok && (debug_bits(err) & kDbgStallMla))
-        ok = warp_wait(smem_u32(&ctl.ml_free), 0, abort_flag, err);
+      if (ok && (debug_bits(err) & kDbgStallMla)) ok = wait32(ctl.ml_free, 0, abort_flag, err);
       while (ok && walk.next(A, p, x)) {
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
           const int sb = tc & 1;
-          if (tc >= 2 &&
-              !(ok = warp_wait(smem_u32(&ctl.s_empty[sb]), ((tc >> 1) + 1) & 1, abort_flag, err)))
+          if (tc >= 2 && !(ok = wait32(ctl.s_empty[sb], ((tc >> 1) + 1) & 1, abort_flag, err)))
             break;
           tc_fence_after();
           const uint32_t d = tmem + 128 * sb;
           const uint32_t id = tile_units(x, t) > 1 ? id2 : id1;
-          for (int ch = 0; ch < 9; ++ch, ++ent) {
-            if (t == p.t0 && ch < kQTmemAtoms) {
-              // Q's chunk has left its place in the ring
-              if (!(ok = warp_wait(smem_u32(&ctl.q_ready[ch]), pieces & 1, abort_flag, err))) break;
-              if (lane == 0) mbar_arrive(smem_u32(&ctl.k_empty[ent % kRing]));
+          const bool first = t == p.t0;
+#pragma unroll 1
+          for (int j = 0; j < kQPairs; ++j, ++ent) {
+            if (first) {                                // Q has left its place in the ring
+              if (!(ok = wait32(ctl.q_ready[j], pieces & 1, abort_flag, err))) break;
+              if (lane == 0) mbar_arrive(smem_u32(&ctl.k_empty[ent & (kRing - 1)]));
               ++ent;
               tc_fence_after();
-            } else if (t == p.t0) {
-              if (!(ok = warp_wait(smem_u32(&ctl.rope_full[pieces & 1]), (pieces >> 1) & 1,
-                                   abort_flag, err)))
-                break;
             }
-            const int st = ent % kRing;
-            if (!(ok = warp_wait(smem_u32(&ctl.k_full[st]), (ent / kRing) & 1, abort_flag, err)))
-              break;
+            const int st = ent & (kRing - 1);
+            if (!(ok = wait32(ctl.k_full[st], (ent / kRing) & 1, abort_flag, err))) break;
+            const uint64_t kd = ring_d + st * (kEntry >> 4);
+            const uint32_t qc = tmem + kColQ + 64 * j;
             if (elect_one()) {
-              const uint64_t kd = sdesc_sw128(smem_u32(sl.ring[st]), 0, 1024);
-              if (ch < kQTmemAtoms) {
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)          // 16 dims: 8 TMEM columns of Q
-                  mma_bf16_ts(d, tmem + kColQ + 32 * ch + 8 * kk, kd + 2 * kk, id,
-                              (ch > 0 || kk > 0) ? 1u : 0u);
-              } else {
-                const uint64_t qd = sdesc_sw128(smem_u32(sl.q_rope[pieces & 1]), 0, 1024);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk) mma_bf16(d, qd + 2 * kk, kd + 2 * kk, id, 1u);
-              }
+              for (int kk = 0; kk < 8; ++kk)            // 16 dims: 8 TMEM columns of Q
+                mma_bf16_ts(d, qc + 8 * kk, kd + (kk >> 2) * (kAtom >> 4) + 2 * (kk & 3), id,
+                            (j > 0 || kk > 0) ? 1u : 0u);
               mma_commit(smem_u32(&ctl.k_empty[st]));
-              if (ch == 8) {
-                mma_commit(smem_u32(&ctl.s_full[sb]));
-                if (t + 1 == p.t1) {
-                  mma_commit(smem_u32(&ctl.q_free));
-                  mma_commit(smem_u32(&ctl.rope_free[pieces & 1]));
-                }
-              }
             }
             __syncwarp();
           }
+          if (!ok) break;
+          if (first && !(ok = wait32(ctl.rope_full, pieces & 1, abort_flag, err))) break;
+          const int st = ent & (kRing - 1);
+          if (!(ok = wait32(ctl.k_full[st], (ent / kRing) & 1, abort_flag, err))) break;
+          ++ent;
+          const uint64_t kd = ring_d + st * (kEntry >> 4);
+          if (elect_one()) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) mma_bf16(d, rope_d + 2 * kk, kd + 2 * kk, id, 1u);
+            mma_commit(smem_u32(&ctl.k_empty[st]));
+            mma_commit(smem_u32(&ctl.s_full[sb]));
+            if (t + 1 == p.t1) mma_commit(smem_u32(&ctl.q_free));
+          }
+          __syncwarp();
         }
         ++pieces;
       }
@@ -547,26 +580,34 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else if (warp == 3) {
       // ----------------------------------------------- P to CTA 1 (CTA 0)
       if (lane == 0) {
-        int a = 0, tc = 0, sent[2] = {0, 0};
+        int a = 0, tc = 0;
+        unsigned sent = 0;                              // parity of each staging's count
         while (ok && walk.next(A, p, x)) {
           for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
-            const int g = tc & 1;
-            for (int u = tile_units(x, t); ok && u > 0; --u, ++a) {
-              const int slot = a & 3;
-              if (!(ok = mbar_wait(smem_u32(&ctl.p_own[g]), sent[g] & 1, abort_flag, err))) break;
-              if (a >= kPSlots && !(ok = mbar_wait<true>(smem_u32(&ctl.p_room[slot]),
-                                                         ((a >> 2) + 1) & 1, abort_flag, err)))
+            const int g = tc & 1, n = tile_units(x, t);
+#pragma unroll 1
+            for (int u = 0; u < n; ++u, ++a) {
+              const int slot = a & 3, bit = 2 * g + u;
+              if (!(ok = wait1(ctl.p_own[g][u], (sent >> bit) & 1, abort_flag, err))) break;
+              if (a >= kPSlots &&
+                  !(ok = wait1<true>(ctl.p_room[slot], ((a >> 2) + 1) & 1, abort_flag, err)))
                 break;
-              bulk_copy_to_peer(mapa(smem_u32(so.p[slot]), peer), smem_u32(sl.p[g]), kPAtom,
+              // The rescale factors go into tile tc - 4's place: p_room says
+              // that PV of the atom four before is done, which is that tile's
+              // or a later one's, and PV waits for its tile's rescale.
+              if (u == 0)
+                bulk_copy_to_peer(mapa(smem_u32(so.alpha[tc & 3]), peer), smem_u32(sl.alpha[g]),
+                                  512, mapa(smem_u32(&ctl.al_full[tc & 3]), peer));
+              bulk_copy_to_peer(mapa(smem_u32(so.p[slot]), peer), smem_u32(sl.p[g][u]), kAtom,
                                 mapa(smem_u32(&ctl.p_full[slot]), peer));
-              ++sent[g];
+              sent ^= 1u << bit;
             }
           }
         }
-        // a copy reads this CTA's staging until it lands
-        for (int g = 0; g < 2; ++g) {
-          if (sent[g] == 0) continue;
-          const uint32_t bar = smem_u32(&ctl.p_ack[g]), parity = (sent[g] - 1) & 1;
+        // a copy reads this CTA's staging until it lands (a staging never
+        // used is in the phase that its parity names as done)
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t bar = smem_u32(&ctl.p_ack[b >> 1][b & 1]), parity = ((sent >> b) & 1) ^ 1;
           if (!mbar_wait<true>(bar, parity, abort_flag, err)) mbar_drain(bar, parity);
         }
       }
@@ -576,7 +617,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const int wq = warp & 3;                          // TMEM lane quarter
       const int r = 32 * wq + lane;                     // row = TMEM lane
       const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
-      int tc = 0, atoms = 0, pieces = 0;
+      int tc = 0, pieces = 0;
+      unsigned acked = 3u;                              // parity of each staging's uses, before the first
       while (ok && walk.next(A, p, x)) {
         const int pos = x.pos0 + r / A.H;
         const int hi = r < x.nrows ? min(pos, x.last) : -1;
@@ -586,11 +628,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int t = p.t0; ok && t < p.t1; ++t) {
           const int n = tile_units(x, t);
           if ((tc & 1) == g) {
-            unsigned long long vis[2] = {0ull, 0ull};
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int un = 2 * t + u;
-              if (un >= x.nu) continue;
+            unsigned long long vis0 = 0ull, vis1 = 0ull;
+            for (int un = 2 * t; un < min(2 * t + 2, x.nu); ++un) {
               const int block = unit_block(x, un);
               bool good = true;
               if (A.block_table) {
@@ -599,119 +638,92 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (!good && lane == 0) raise_error(err, kErrBounds);
               }
               const int kb = block * 64;
-              if (good) vis[u] = range_bits(lo - kb, hi - kb) | range_bits(0, sink_hi - kb);
+              const unsigned long long see =
+                  good ? range_bits(lo - kb, hi - kb) | range_bits(0, sink_hi - kb) : 0ull;
+              if (un & 1)
+                vis1 = see;
+              else
+                vis0 = see;
             }
-            if (!(ok = warp_wait(smem_u32(&ctl.s_full[g]), (tc >> 1) & 1, abort_flag, err))) break;
+            if (!(ok = wait32(ctl.s_full[g], (tc >> 1) & 1, abort_flag, err))) break;
             tc_fence_after();
             const uint32_t s_cols = tmem + lanes + 128 * g;
             float mx = -INFINITY;
+#pragma unroll 1
+            for (int u = 0; u < n; ++u) {
+              float s[64];
+              tmem_ld64(s_cols + 64 * u, s);
+              const unsigned long long see = u ? vis1 : vis0;
+              if (!__all_sync(0xffffffffu, see == ~0ull)) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (u >= n) continue;
-              float pm[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-              const bool all = __all_sync(0xffffffffu, vis[u] == ~0ull);
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float s[32];
-                tmem_ld32(s_cols + 64 * u + 32 * h, s);
-                if (all) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) pm[e & 3] = fmaxf(pm[e & 3], s[e]);
-                } else {
-                  const unsigned bits = static_cast<unsigned>(vis[u] >> (32 * h));
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    pm[e & 3] = fmaxf(pm[e & 3], (bits >> e) & 1u ? s[e] : -INFINITY);
-                }
+                for (int e = 0; e < 64; ++e)
+                  if (!((see >> e) & 1ull)) s[e] = -INFINITY;
               }
-              mx = fmaxf(mx, fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])));
+              float pm[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int e = 0; e < 64; ++e) pm[e & 3] = fmaxf(pm[e & 3], s[e]);
+              mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
             }
             mx *= A.sm_scale_log2;
             // the other group's reference maximum of the tile before
-            if (tc > 0 &&
-                !(ok = warp_wait(smem_u32(&ctl.m_bar[wq]), (tc - 1) & 1, abort_flag, err)))
-              break;
+            if (tc > 0 && !(ok = wait32(ctl.m_bar[wq], (tc - 1) & 1, abort_flag, err))) break;
             const bool first = t == p.t0;
-            const float m_prev = first ? -INFINITY : ctl.m[(tc + 1) & 1][r];
+            const float m_prev = first ? -INFINITY : sl.m[(tc + 1) & 1][r];
             const float m_new = mx > m_prev + kRebase ? mx : m_prev;
-            ctl.m[tc & 1][r] = m_new;
+            sl.m[tc & 1][r] = m_new;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.m_bar[wq]));
             const bool re = m_prev > -INFINITY && m_new != m_prev;
-            const bool any = __any_sync(0xffffffffu, re);
             if (m_own > -INFINITY && m_own != m_new) l *= fast_exp2(m_own - m_new);
             m_own = m_new;
             const float base = m_new == -INFINITY ? 0.f : m_new;
+#pragma unroll 1
+            for (int u = 0; u < n; ++u) {
+              float s[64];
+              tmem_ld64(s_cols + 64 * u, s);
+              if (u + 1 == n) {                         // the buffer is free for another tile
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl.s_empty[g]));
+              }
+              const unsigned long long see = u ? vis1 : vis0;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              if (u >= n) continue;
+              for (int e = 0; e < 64; ++e) s[e] = fast_exp2(fmaf(s[e], A.sm_scale_log2, -base));
+              if (!__all_sync(0xffffffffu, see == ~0ull)) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                  if (!((see >> e) & 1ull)) s[e] = 0.f;
+              }
               float ps[4] = {0.f, 0.f, 0.f, 0.f};
               uint32_t pk[32];
-              const bool all = __all_sync(0xffffffffu, vis[u] == ~0ull);
 #pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float s[32];
-                tmem_ld32(s_cols + 64 * u + 32 * h, s);
-                if (h == 1 && u + 1 == n) {             // the buffer is free for another tile
-                  tc_fence_before();
-                  __syncwarp();
-                  if (lane == 0) mbar_arrive(smem_u32(&ctl.s_empty[g]));
-                }
-                if (all) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    s[e] = fast_exp2(fmaf(s[e], A.sm_scale_log2, -base));
-                } else {
-                  const unsigned bits = static_cast<unsigned>(vis[u] >> (32 * h));
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    s[e] = (bits >> e) & 1u ? fast_exp2(fmaf(s[e], A.sm_scale_log2, -base)) : 0.f;
-                }
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  ps[e & 3] += s[2 * e] + s[2 * e + 1];
-                  const __nv_bfloat162 pb = __floats2bfloat162_rn(s[2 * e], s[2 * e + 1]);
-                  pk[16 * h + e] = *reinterpret_cast<const uint32_t*>(&pb);
-                }
+              for (int e = 0; e < 32; ++e) {
+                ps[e & 3] += s[2 * e] + s[2 * e + 1];
+                const __nv_bfloat162 pb = __floats2bfloat162_rn(s[2 * e], s[2 * e + 1]);
+                pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
               }
               l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-              if (atoms > 0 && !(ok = warp_wait<true>(smem_u32(&ctl.p_ack[g]), (atoms - 1) & 1,
-                                                      abort_flag, err)))
-                break;
-              ++atoms;
-              if (u == 0) {
-                // Rescale factors of this tile tc, in the slot of tile tc - 4.
-                // CTA 1 has read that one: the last atom of tile tc - 2 has
-                // landed there (the wait above), in the place of the atom
-                // four before, which PV freed after its tile's rescale and
-                // which is tile tc - 4's or later, unless tiles tc - 3 and
-                // tc - 2 both ended a piece; then ml_free has let this warp
-                // pass only after CTA 1 was done with tile tc - 3.
-                if (any) st_cluster_f32(mapa(smem_u32(&so.alpha[tc & 3][r]), peer),
-                                        re ? fast_exp2(m_prev - m_new) : 1.f);
-                if (lane == 0)
-                  st_cluster_f32(mapa(smem_u32(&ctl.flag[tc & 3][wq]), peer),
-                                 __uint_as_float(any ? 1u : 0u));
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctl.al_full[tc & 3]), peer));
-              }
+              // the staging is free once CTA 1 holds what it held (a barrier not
+              // yet used passes for the phase before its first)
+              if (!(ok = wait32<true>(ctl.p_ack[g][u], (acked >> u) & 1, abort_flag, err))) break;
+              acked ^= 1u << u;
+              if (u == 0) sl.alpha[g][r] = re ? fast_exp2(m_prev - m_new) : 1.f;
               // row r of the atom: 128 B, 16-B chunk c at chunk c ^ (r % 8)
-              uint4* row = reinterpret_cast<uint4*>(sl.p[g] + r * 128);
+              uint4* row = reinterpret_cast<uint4*>(sl.p[g][u] + r * 128);
 #pragma unroll
               for (int c = 0; c < 8; ++c)
                 row[c ^ (r & 7)] =
                     make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
               fence_proxy_async_smem();                 // generic writes -> bulk-copy reads
               __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&ctl.p_own[g]));
+              if (lane == 0) mbar_arrive(smem_u32(&ctl.p_own[g][u]));
             }
           }
           ++tc;
         }
         if (!ok) break;
         // the group's maximum and sum go to CTA 1
-        if (pieces > 0 && !(ok = warp_wait<true>(smem_u32(&ctl.ml_free), (pieces - 1) & 1,
-                                                 abort_flag, err)))
+        if (pieces > 0 && !(ok = wait32<true>(ctl.ml_free, (pieces - 1) & 1, abort_flag, err)))
           break;
         const uint32_t ml = mapa(smem_u32(&so.ml[g][r]), peer);
         st_cluster_f32(ml, m_own);
@@ -735,8 +747,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             r1 = unit_row(A, x, 2 * t + 3);
             for (int h = 0; h < 2 * n; ++h, ++vc) {
               const int st = vc & 3;
-              if (vc >= kVRing && !(ok = mbar_wait(smem_u32(&ctl.v_empty[st]), ((vc >> 2) + 1) & 1,
-                                                   abort_flag, err)))
+              if (vc >= kVRing &&
+                  !(ok = wait1(ctl.v_empty[st], ((vc >> 2) + 1) & 1, abort_flag, err)))
                 break;
               const uint32_t full = smem_u32(&ctl.v_full[st]);
               mbar_expect_tx(full, kVChunk);
@@ -751,24 +763,24 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     } else if (warp == 1) {
       // ------------------------------------------------------- PV (CTA 1)
       const uint32_t id = idesc_bf16(128, 256, true);
+      const uint64_t p_d = sdesc_sw128(smem_u32(so.p[0]), 0, 1024);
+      const uint64_t v_d = sdesc_sw128(smem_u32(so.v[0]), kUnitAtom, 1024);
       int vc = 0, tc = 0, ac = 0;
       while (ok && walk.next(A, p, x)) {
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
           const int n = tile_units(x, t);
-          if (!(ok = warp_wait(smem_u32(&ctl.o_ok[tc & 3]), (tc >> 2) & 1, abort_flag, err))) break;
+          if (!(ok = wait32(ctl.o_ok[tc & 3], (tc >> 2) & 1, abort_flag, err))) break;
           tc_fence_after();
           for (int u = 0; ok && u < n; ++u, ++ac) {
             const int slot = ac & 3;
-            if (!(ok = warp_wait<true>(smem_u32(&ctl.p_full[slot]), (ac >> 2) & 1, abort_flag,
-                                       err)))
-              break;
+            if (!(ok = wait32<true>(ctl.p_full[slot], (ac >> 2) & 1, abort_flag, err))) break;
+            const uint64_t pd = p_d + slot * (kAtom >> 4);
+#pragma unroll 1
             for (int h = 0; h < 2; ++h, ++vc) {
               const int st = vc & 3;
-              if (!(ok = warp_wait(smem_u32(&ctl.v_full[st]), (vc >> 2) & 1, abort_flag, err)))
-                break;
+              if (!(ok = wait32(ctl.v_full[st], (vc >> 2) & 1, abort_flag, err))) break;
+              const uint64_t vd = v_d + st * (kVChunk >> 4);
               if (elect_one()) {
-                const uint64_t pd = sdesc_sw128(smem_u32(so.p[slot]), 0, 1024);
-                const uint64_t vd = sdesc_sw128(smem_u32(so.v[st]), kUnitChunk, 1024);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)          // 16 keys: 32 B of P, 2 KB of V
                   mma_bf16(tmem + 256 * h, pd + 2 * kk, vd + (kk * 2048 >> 4), id,
@@ -800,17 +812,19 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         int a = 0, tc = 0;
         while (ok && walk.next(A, p, x)) {
           for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
-            for (int u = tile_units(x, t); ok && u > 0; --u, ++a) {
+            const int n = tile_units(x, t);
+#pragma unroll 1
+            for (int u = 0; u < n; ++u, ++a) {
               const int slot = a & 3;
               if (warp == 2) {
-                if (!(ok = mbar_wait<true>(smem_u32(&ctl.p_full[slot]), (a >> 2) & 1, abort_flag,
-                                           err)))
+                if (u == 0 &&
+                    !(ok = wait1<true>(ctl.al_full[tc & 3], (tc >> 2) & 1, abort_flag, err)))
                   break;
-                mbar_arrive_remote(mapa(smem_u32(&ctl.p_ack[tc & 1]), peer));
+                if (!(ok = wait1<true>(ctl.p_full[slot], (a >> 2) & 1, abort_flag, err))) break;
+                mbar_arrive_remote(mapa(smem_u32(&ctl.p_ack[tc & 1][u]), peer));
               } else {
-                if (!(ok = mbar_wait(smem_u32(&ctl.p_free[slot]), (a >> 2) & 1, abort_flag, err)))
-                  break;
-                mbar_expect_tx(smem_u32(&ctl.p_full[slot]), kPAtom);
+                if (!(ok = wait1(ctl.p_free[slot], (a >> 2) & 1, abort_flag, err))) break;
+                mbar_expect_tx(smem_u32(&ctl.p_full[slot]), kAtom);
                 mbar_arrive_remote(mapa(smem_u32(&ctl.p_room[slot]), peer));
               }
             }
@@ -839,8 +853,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
           // (every tile's chunks are waited for, so that no phase is missed)
           for (int c = vc; ok && c < vc + 2 * n; ++c) {
-            if (!(ok = warp_wait(smem_u32(&ctl.v_full[c & 3]), (c >> 2) & 1, abort_flag, err)))
-              break;
+            if (!(ok = wait32(ctl.v_full[c & 3], (c >> 2) & 1, abort_flag, err))) break;
             if (edge) {
               uint4* v = reinterpret_cast<uint4*>(so.v[c & 3]);
               auto clean = [](uint32_t w) {
@@ -858,13 +871,12 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           if (!ok) break;
           if (edge) fence_proxy_async_smem();
           vc += 2 * n;
-          if (!(ok = warp_wait<true>(smem_u32(&ctl.al_full[sl4]), (tc >> 2) & 1, abort_flag, err)))
-            break;
-          if (ctl.flag[sl4][wq]) {
-            const float alpha = so.alpha[sl4][r];
+          if (!(ok = wait32<true>(ctl.al_full[sl4], (tc >> 2) & 1, abort_flag, err))) break;
+          if (threadIdx.x == 128) mbar_expect_tx(smem_u32(&ctl.al_full[sl4]), 512);
+          const float alpha = so.alpha[sl4][r];
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
             // never on a piece's first tile, so the PV of the tile before is this piece's
-            if (!(ok = warp_wait(smem_u32(&ctl.pv_done[(tc + 3) & 3]), ((tc - 1) >> 2) & 1,
-                                 abort_flag, err)))
+            if (!(ok = wait32(ctl.pv_done[(tc + 3) & 3], ((tc - 1) >> 2) & 1, abort_flag, err)))
               break;
             tc_fence_after();
 #pragma unroll 1
@@ -882,14 +894,14 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (!ok) break;
         // ------------------------------------------------------- a piece's end
-        if (!(ok = warp_wait<true>(smem_u32(&ctl.ml_full), pieces & 1, abort_flag, err))) break;
+        if (!(ok = wait32<true>(ctl.ml_full, pieces & 1, abort_flag, err))) break;
         const float2 a0 = so.ml[0][r], a1 = so.ml[1][r];
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctl.ml_free), peer));
         const float m = fmaxf(a0.x, a1.x);
         const float l = (a0.x > -INFINITY ? a0.y * fast_exp2(a0.x - m) : a0.y) +
                         (a1.x > -INFINITY ? a1.y * fast_exp2(a1.x - m) : a1.y);
-        if (!(ok = warp_wait(smem_u32(&ctl.o_done), pieces & 1, abort_flag, err))) break;
+        if (!(ok = wait32(ctl.o_done, pieces & 1, abort_flag, err))) break;
         tc_fence_after();
         const bool valid = r < x.nrows;
         if (p.first && p.last) {
