@@ -75,9 +75,10 @@ struct OutputSmem {                             // CTA 1
   uint8_t v[kVRing][kVChunk];
   float alpha[4][128];                          // rescale factors, by tile
   float2 ml[2][128];                            // maximum and sum of each softmax group
+  uint8_t stage[8][32 * 64];                    // output rows on their way out, by warp
 };
-constexpr size_t kBig = sizeof(LogitsSmem);
-static_assert(sizeof(OutputSmem) <= kBig && kBig % 1024 == 0, "both roles fit");
+constexpr size_t kBig = std::max(sizeof(LogitsSmem), sizeof(OutputSmem));
+static_assert(kBig % 1024 == 0, "the control block follows the larger role's memory");
 
 struct Ctl {
   // CTA 0
@@ -335,6 +336,23 @@ __device__ __forceinline__ unsigned long long range_bits(int a, int b) {
   b = min(b, 63);
   if (a > b) return 0ull;
   return (~0ull >> (63 - b)) & (~0ull << a);
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -677,47 +695,58 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (m_own > -INFINITY && m_own != m_new) l *= fast_exp2(m_own - m_new);
             m_own = m_new;
             const float base = m_new == -INFINITY ? 0.f : m_new;
+            const float2 scale2 = make_float2(A.sm_scale_log2, A.sm_scale_log2);
+            const float2 base2 = make_float2(-base, -base);
+            float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll 1
             for (int u = 0; u < n; ++u) {
-              float s[64];
-              tmem_ld64(s_cols + 64 * u, s);
-              if (u + 1 == n) {                         // the buffer is free for another tile
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl.s_empty[g]));
-              }
-              const unsigned long long see = u ? vis1 : vis0;
-#pragma unroll
-              for (int e = 0; e < 64; ++e) s[e] = fast_exp2(fmaf(s[e], A.sm_scale_log2, -base));
-              if (!__all_sync(0xffffffffu, see == ~0ull)) {
-#pragma unroll
-                for (int e = 0; e < 64; ++e)
-                  if (!((see >> e) & 1ull)) s[e] = 0.f;
-              }
-              float ps[4] = {0.f, 0.f, 0.f, 0.f};
-              uint32_t pk[32];
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                ps[e & 3] += s[2 * e] + s[2 * e + 1];
-                const __nv_bfloat162 pb = __floats2bfloat162_rn(s[2 * e], s[2 * e + 1]);
-                pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
-              }
-              l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
               // the staging is free once CTA 1 holds what it held (a barrier not
               // yet used passes for the phase before its first)
               if (!(ok = wait32<true>(ctl.p_ack[g][u], (acked >> u) & 1, abort_flag, err))) break;
               acked ^= 1u << u;
               if (u == 0) sl.alpha[g][r] = re ? fast_exp2(m_prev - m_new) : 1.f;
-              // row r of the atom: 128 B, 16-B chunk c at chunk c ^ (r % 8)
-              uint4* row = reinterpret_cast<uint4*>(sl.p[g][u] + r * 128);
+              uint8_t* row = sl.p[g][u] + r * 128;
+#pragma unroll 1
+              for (int h = 0; h < 2; ++h) {
+                float s[32];
+                tmem_ld32(s_cols + 64 * u + 32 * h, s);
+                const unsigned bits = static_cast<unsigned>((u ? vis1 : vis0) >> (32 * h));
 #pragma unroll
-              for (int c = 0; c < 8; ++c)
-                row[c ^ (r & 7)] =
-                    make_uint4(pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+                for (int e = 0; e < 16; ++e) {
+                  const float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), scale2, base2);
+                  s[2 * e] = fast_exp2(z.x);
+                  s[2 * e + 1] = fast_exp2(z.y);
+                }
+                if (!__all_sync(0xffffffffu, bits == ~0u)) {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if (!((bits >> e) & 1u)) s[e] = 0.f;
+                }
+                // row r of the atom: 128 B, 16-B chunk c at chunk c ^ (r % 8)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t pk[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) {
+                    const float2 v = make_float2(s[8 * c + 2 * e], s[8 * c + 2 * e + 1]);
+                    sum2 = add2(sum2, v);
+                    const __nv_bfloat162 pb = __floats2bfloat162_rn(v.x, v.y);
+                    pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
+                  }
+                  *reinterpret_cast<uint4*>(row + (((4 * h + c) ^ (r & 7)) << 4)) =
+                      make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                }
+              }
+              if (u + 1 == n) {                         // the buffer is free for another tile
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&ctl.s_empty[g]));
+              }
               fence_proxy_async_smem();                 // generic writes -> bulk-copy reads
               __syncwarp();
               if (lane == 0) mbar_arrive(smem_u32(&ctl.p_own[g][u]));
             }
+            l += sum2.x + sum2.y;
           }
           ++tc;
         }
@@ -906,24 +935,37 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const bool valid = r < x.nrows;
         if (p.first && p.last) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
-          __nv_bfloat16* orow = A.out + (x.row0 + r) * 512 + 256 * g;
+          // 32 dims at a time through shared memory (row of 64 B, 16-B chunk c
+          // at c ^ (row / 2 % 4)), so that a warp's store covers whole sectors
+          uint8_t* mine = so.stage[warp - 4];
+          const int sub = lane & 3, row0 = lane >> 2;
+          __nv_bfloat16* out = A.out + (x.row0 + 32 * wq) * 512 + 256 * g + 8 * sub;
 #pragma unroll 1
           for (int cc = 0; cc < 8; ++cc) {
             float o[32];
             tmem_ld32(o_cols + 32 * cc, o);
-            if (!valid) continue;
-            uint4* dst = reinterpret_cast<uint4*>(orow + 32 * cc);
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
+            for (int c = 0; c < 4; ++c) {
               uint32_t w[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * q4 + 2 * e] * inv,
-                                                               o[8 * q4 + 2 * e + 1] * inv);
+                const __nv_bfloat162 v = __floats2bfloat162_rn(o[8 * c + 2 * e] * inv,
+                                                               o[8 * c + 2 * e + 1] * inv);
                 w[e] = *reinterpret_cast<const uint32_t*>(&v);
               }
-              dst[q4] = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(mine + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
             }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const int row = row0 + 8 * k;
+              const uint4 v = *reinterpret_cast<const uint4*>(
+                  mine + row * 64 + ((sub ^ ((row >> 1) & 3)) << 4));
+              if (32 * wq + row < x.nrows)
+                *reinterpret_cast<uint4*>(out + static_cast<long long>(row) * 512 + 32 * cc) = v;
+            }
+            __syncwarp();
           }
           if (g == 0 && valid && A.lse)
             A.lse[x.row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
