@@ -56,7 +56,7 @@ constexpr int kQPairs = 4;                      // Q dims [0, 512) live in TMEM,
 constexpr uint32_t kColQ = 256;                 // after two buffers of 128 logits
 constexpr int kPSlots = 4;
 constexpr int kVRing = 4;
-constexpr int kAhead = 3;                       // tiles of L2 prefetch
+constexpr int kAhead = 6;                       // tiles of L2 prefetch, ahead of CTA 1
 constexpr float kRebase = 8.0f;                 // lazy rescale threshold (log2 units)
 constexpr int kMaxClusters = 74;                // two CTAs on each of 148 SMs
 constexpr int kScanItems = 16384;               // row tiles a cluster scans for its share
@@ -433,17 +433,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (lane == 0) {
         int ent = 0, pieces = 0;
         while (ok && walk.next(A, p, x)) {
-          auto prefetch_tile = [&](int t) {
-            if (t >= p.t1) return;
-            for (int u = 2 * t; u < min(2 * t + 2, x.nu); ++u) {
-              const int row = unit_row(A, x, u);
-              if (row < A.kv_rows)
-                prefetch_l2(A.kv + static_cast<long long>(row) * 576,
-                            1152u * static_cast<unsigned>(min(64, A.kv_rows - row)));
-            }
-          };
-          if (par == 0)
-            for (int t = 1; t < kAhead; ++t) prefetch_tile(p.t0 + t);
           const int q_row = static_cast<int>(x.row0);
           int r0 = unit_row(A, x, 2 * p.t0), r1 = unit_row(A, x, 2 * p.t0 + 1);
           for (int t = p.t0; ok && t < p.t1; ++t) {
@@ -451,7 +440,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int c0 = r0, c1 = r1;
             r0 = unit_row(A, x, 2 * t + 2);
             r1 = unit_row(A, x, 2 * t + 3);
-            if (par == 0) prefetch_tile(t + kAhead);
             const bool with_q = t == p.t0;
             const int count = with_q ? 5 + kQPairs : 5;
 #pragma unroll 1
@@ -550,6 +538,10 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           const uint32_t d = tmem + 128 * sb;
           const uint32_t id = tile_units(x, t) > 1 ? id2 : id1;
           const bool first = t == p.t0;
+          // an entry's barrier is asked for before the MMAs of the one before
+          // it are issued, so that a satisfied wait costs nothing after them
+          bool there = !first && mbar_try_wait(smem_u32(&ctl.k_full[ent & (kRing - 1)]),
+                                               (ent / kRing) & 1);
 #pragma unroll 1
           for (int j = 0; j < kQPairs; ++j, ++ent) {
             if (first) {                                // Q has left its place in the ring
@@ -559,7 +551,12 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               tc_fence_after();
             }
             const int st = ent & (kRing - 1);
-            if (!(ok = wait32(ctl.k_full[st], (ent / kRing) & 1, abort_flag, err))) break;
+            if (!__all_sync(0xffffffffu, there) &&
+                !(ok = wait32(ctl.k_full[st], (ent / kRing) & 1, abort_flag, err)))
+              break;
+            there = (!first || j + 1 == kQPairs) &&
+                    mbar_try_wait(smem_u32(&ctl.k_full[(ent + 1) & (kRing - 1)]),
+                                  ((ent + 1) / kRing) & 1);
             const uint64_t kd = ring_d + st * (kEntry >> 4);
             const uint32_t qc = tmem + kColQ + 64 * j;
             if (elect_one()) {
@@ -574,7 +571,9 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           if (!ok) break;
           if (first && !(ok = wait32(ctl.rope_full, pieces & 1, abort_flag, err))) break;
           const int st = ent & (kRing - 1);
-          if (!(ok = wait32(ctl.k_full[st], (ent / kRing) & 1, abort_flag, err))) break;
+          if (!__all_sync(0xffffffffu, there) &&
+              !(ok = wait32(ctl.k_full[st], (ent / kRing) & 1, abort_flag, err)))
+            break;
           ++ent;
           const uint64_t kd = ring_d + st * (kEntry >> 4);
           if (elect_one()) {
@@ -767,13 +766,29 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // ---------------------------------------------------- V loads (CTA 1)
       if (lane == 0) {
         int vc = 0;
+        // brings a unit into L2 (row kv_rows: none)
+        auto prefetch = [&](int row) {
+          if (row < A.kv_rows)
+            prefetch_l2(A.kv + static_cast<long long>(row) * 576,
+                        1152u * static_cast<unsigned>(min(64, A.kv_rows - row)));
+        };
         while (ok && walk.next(A, p, x)) {
+          for (int u = 2 * p.t0 + 2; u < min(2 * (p.t0 + kAhead), 2 * p.t1); ++u)
+            prefetch(unit_row(A, x, u));
+          // table entries are loaded a tile before they are used
+          const int u_end = min(2 * p.t1, x.nu);
+          auto ahead = [&](int u) { return u < u_end ? unit_row(A, x, u) : A.kv_rows; };
           int r0 = unit_row(A, x, 2 * p.t0), r1 = unit_row(A, x, 2 * p.t0 + 1);
+          int f0 = ahead(2 * (p.t0 + kAhead)), f1 = ahead(2 * (p.t0 + kAhead) + 1);
           for (int t = p.t0; ok && t < p.t1; ++t) {
             const int n = tile_units(x, t);
-            const int c0 = r0, c1 = r1;
+            const int c0 = r0, c1 = r1, d0 = f0, d1 = f1;
             r0 = unit_row(A, x, 2 * t + 2);
             r1 = unit_row(A, x, 2 * t + 3);
+            f0 = ahead(2 * (t + 1 + kAhead));
+            f1 = ahead(2 * (t + 1 + kAhead) + 1);
+            prefetch(d0);
+            prefetch(d1);
             for (int h = 0; h < 2 * n; ++h, ++vc) {
               const int st = vc & 3;
               if (vc >= kVRing &&
