@@ -173,6 +173,8 @@ struct MassArgs {
   float* mass = nullptr;                  // [B][ld]
   long long ld = 0;
   unsigned* err = nullptr;
+  // filled by the launcher: row tiles of G queries, per_seq a sequence
+  int G = 0, per_seq = 0, kv_rows = 0, box_rows = 0;
 };
 
 struct EvictArgs {

@@ -40,6 +40,7 @@
 
 #include "common.cuh"
 #include "dsa_internal.h"
+#include "split.cuh"
 
 namespace dsa {
 namespace {
@@ -101,9 +102,7 @@ struct Ctl {
   unsigned long long pv_done[4];
   unsigned long long o_done;
   unsigned long long ml_full;
-  // the cluster's share of the work
-  long long total, start;                       // all weight; the weight before the share
-  int item, off, left, nc;                      // first row tile, offset into it, weight, clusters
+  Share share;                                  // of the row tiles' weights
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -191,8 +190,8 @@ struct Piece {
 struct Walk {
   int item, off, left;
   long long start;
-  __device__ __forceinline__ Walk(const Ctl& c)
-      : item(c.item), off(c.off), left(c.left), start(c.start) {}
+  __device__ __forceinline__ Walk(const Share& s)
+      : item(s.item), off(s.off), left(s.left), start(s.start) {}
   // Out of line: every role calls it, once a piece.
   __device__ __noinline__ bool step(const RangeArgs& A, Piece& p, Item& x) {
     if (A.whole) {
@@ -235,100 +234,6 @@ struct Walk {
   }
 };
 
-// The bounded waits of common.cuh with the slow path out of line: this kernel
-// has some thirty of them in sixteen warps that run different code, and short
-// loops that have to fit the instruction caches.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                       unsigned* err) {
-  return mbar_wait<true>(bar, parity, abort_flag, err);
-}
-template <bool kCluster = false>
-__device__ __forceinline__ bool wait1(unsigned long long& b, uint32_t parity,
-                                      volatile int* abort_flag, unsigned* err) {
-  const uint32_t bar = smem_u32(&b);
-  if (kCluster ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
-  return wait_slow(bar, parity, abort_flag, err);
-}
-// By every lane of a warp, which agrees on the result.
-template <bool kCluster = false>
-__device__ __forceinline__ bool wait32(unsigned long long& b, uint32_t parity,
-                                       volatile int* abort_flag, unsigned* err) {
-  return __all_sync(0xffffffffu, wait1<kCluster>(b, parity, abort_flag, err));
-}
-
-__device__ __forceinline__ long long share_begin(long long total, int nc, int c) {
-  return total * c / nc;
-}
-
-// Finds this cluster's share: the weights of all row tiles are added up and
-// cut into equal parts. `sums` is scratch for one number a thread.
-__device__ void find_share(const RangeArgs& A, Ctl& ctl, long long* sums, int cluster) {
-  const int tid = static_cast<int>(threadIdx.x);
-  if (A.whole) {
-    if (tid == 0) {
-      ctl.item = cluster;
-      ctl.off = ctl.left = 0;
-      ctl.start = 0;
-    }
-    return;
-  }
-  const int per = (A.items + kThreads - 1) / kThreads;
-  const int i0 = min(A.items, tid * per), i1 = min(A.items, i0 + per);
-  long long sum = 0;
-  for (int i = i0; i < i1; ++i) {
-    if (A.block_table && blockIdx.x == 0) {
-      const int len = A.seq_len[i / A.per_seq];
-      if (len < 0 || len > A.max_blocks * 64) raise_error(A.err, kErrBounds);
-    }
-    sum += item_geom(A, i).tiles + kItemCost;
-  }
-  sums[tid] = sum;
-  if (tid == 0) {
-    ctl.item = A.items;
-    ctl.off = ctl.left = 0;
-    ctl.start = 0;
-  }
-  __syncthreads();
-  if (tid < 32) {
-    long long mine = 0;
-    for (int k = 0; k < kThreads / 32; ++k) mine += sums[tid * (kThreads / 32) + k];
-    long long before = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, before, o);
-      if (tid >= o) before += y;
-    }
-    if (tid == 31) ctl.total = before;
-    before -= mine;
-    for (int k = 0; k < kThreads / 32; ++k) {
-      const long long v = sums[tid * (kThreads / 32) + k];
-      sums[tid * (kThreads / 32) + k] = before;
-      before += v;
-    }
-  }
-  __syncthreads();
-  const long long total = ctl.total;
-  const int nc = static_cast<int>(
-      max(1ll, min(static_cast<long long>(A.clusters), total / kMinShare)));
-  if (tid == 0) ctl.nc = nc;
-  if (cluster >= nc) return;
-  const long long w0 = share_begin(total, nc, cluster), w1 = share_begin(total, nc, cluster + 1);
-  if (sums[tid] <= w0 && w0 < sums[tid] + sum) {
-    long long at = sums[tid];
-    for (int i = i0; i < i1; ++i) {
-      const int weight = item_geom(A, i).tiles + kItemCost;
-      if (w0 < at + weight) {
-        ctl.item = i;
-        ctl.off = static_cast<int>(w0 - at);
-        ctl.left = static_cast<int>(w1 - w0);
-        ctl.start = at;
-        break;
-      }
-      at += weight;
-    }
-  }
-}
-
 // Bits of the 64 keys from kb on that a row with positions [lo, hi] and the
 // first `sinks` keys sees.
 __device__ __forceinline__ unsigned long long range_bits(int a, int b) {
@@ -370,7 +275,21 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const int cluster = static_cast<int>(blockIdx.x >> 1);
   const int warp = warp_id(), lane = lane_id();
 
-  find_share(A, ctl, reinterpret_cast<long long*>(big), cluster);
+  if (A.whole) {
+    if (threadIdx.x == 0) {
+      ctl.share = Share{};
+      ctl.share.item = cluster;
+    }
+  } else {
+    find_share<kThreads>(ctl.share, reinterpret_cast<long long*>(big), A.items, cluster,
+                         A.clusters, kMinShare, [&](int i) {
+                           if (A.block_table && blockIdx.x == 0) {
+                             const int len = A.seq_len[i / A.per_seq];
+                             if (len < 0 || len > A.max_blocks * 64) raise_error(err, kErrBounds);
+                           }
+                           return item_geom(A, i).tiles + kItemCost;
+                         });
+  }
   if (threadIdx.x == 0) {
     auto init = [](unsigned long long& b, int count) { mbar_init(smem_u32(&b), count); };
     init(ctl.q_free, 1);
@@ -418,7 +337,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   volatile int* abort_flag = &ctl.abort_flag;
-  Walk walk(ctl);
+  Walk walk(ctl.share);
   Piece p;
   Item x;
   bool ok = *abort_flag == 0;
@@ -1002,9 +921,11 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           if (g == 0 && valid) A.part_ml[slot * A.rows_pad + r] = make_float2(m, l);
           if (p.first && threadIdx.x == 128) {
             const long long at = p.start + kItemCost + x.tiles - 1;
-            int e = static_cast<int>(at * ctl.nc / ctl.total);
-            while (e + 1 < ctl.nc && share_begin(ctl.total, ctl.nc, e + 1) <= at) ++e;
-            while (e > 0 && share_begin(ctl.total, ctl.nc, e) > at) --e;
+            const long long total = ctl.share.total;
+            const int parts = ctl.share.parts;
+            int e = static_cast<int>(at * parts / total);
+            while (e + 1 < parts && share_begin(total, parts, e + 1) <= at) ++e;
+            while (e > 0 && share_begin(total, parts, e) > at) --e;
             A.rec[cluster] = make_int2(p.item, e);
             recorded = true;
           }
