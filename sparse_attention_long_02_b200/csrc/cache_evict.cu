@@ -6,13 +6,20 @@
 // running totals (ties to the smaller slot). The kept rows move, in order, to
 // the sequence's slots 0 .. budget-1, in place.
 //
-// evict_select_kernel, one CTA per sequence: a radix select (four 8-bit
-// digits) of the threshold total, then one ordered pass that writes the kept
-// slots. evict_move_kernel: a row's destination is never behind its source
-// slot, so a CTA that walks the kept rows in order, reading a chunk of rows
-// before it writes them, never overwrites a row it has still to read. The
-// bytes of a row are split over CTAs by column, each CTA moving its columns of
-// every row: no CTA reads what another one writes.
+// evict_select_kernel, a cluster of 1 to 8 CTAs per sequence: a radix select
+// (11 + 11 + 10 bits) of the threshold total over histograms that the CTAs add
+// up through distributed shared memory. With `ties` the number of totals equal
+// to the threshold that are kept, slot i's place is
+//   (kept for certain before i) + min(ties, equal before i),
+// so one counting pass and one writing pass over each warp's own run of slots
+// give the kept slots in order without a scan per step.
+//
+// evict_move_kernel: a row's destination is never behind its source slot, so a
+// CTA that walks the kept rows in order, reading a step's rows before it writes
+// them, never overwrites a row it has still to read (nor one of the next step,
+// which it reads ahead). The bytes of a row are split over CTAs by column, each
+// moving its columns of every row: no CTA reads what another one writes. Bound
+// by HBM, each moved byte read and written once.
 #include "common.cuh"
 #include "dsa_internal.h"
 
@@ -20,7 +27,10 @@ namespace dsa {
 namespace {
 
 constexpr int kSelThreads = 1024;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelKeys = 40960;                 // keys a CTA keeps in shared memory
 constexpr int kMoveThreads = 512;
+constexpr int kMoveRows = 4;                    // rows a thread moves in one step
 
 // Order-preserving key of a total; NaN below everything, -0 equal to +0.
 __device__ __forceinline__ unsigned total_key(float v) {
@@ -29,164 +39,294 @@ __device__ __forceinline__ unsigned total_key(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive prefix of v over the block, total in *sum.
-__device__ __forceinline__ int block_prefix(int v, int* warp_sums, int* sum) {
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane_id() >= o) x += y;
-  }
-  if (lane_id() == 31) warp_sums[warp_id()] = x;
-  __syncthreads();
-  if (warp_id() == 0) {
-    int w = warp_sums[lane_id()];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane_id() >= o) w += y;
-    }
-    warp_sums[lane_id()] = w;
-  }
-  __syncthreads();
-  const int before = warp_id() ? warp_sums[warp_id() - 1] : 0;
-  *sum = warp_sums[31];
-  __syncthreads();
-  return before + x - v;
+struct SelSmem {
+  unsigned hist[4][2048];                       // by lane % 4; [0] then holds the CTA's sum
+  int warp_above[kSelWarps], warp_eq[kSelWarps];
+  int above, eq;                                // the CTA's counts
+  unsigned scan[kSelWarps];
+  unsigned digit, left;
+  unsigned skip;                                // a timeout is recorded: do nothing
+};
+
+__device__ __forceinline__ unsigned cluster_size() {
+  unsigned n;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
+  return n;
+}
+__device__ __forceinline__ unsigned ld_cluster(uint32_t addr) {
+  unsigned v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs A) {
-  __shared__ unsigned hist[256];
-  __shared__ unsigned s_prefix, s_want;
-  __shared__ int warp_sums[32];
-  const int b = static_cast<int>(blockIdx.x);
-  const int tid = static_cast<int>(threadIdx.x);
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SelSmem& sm = *reinterpret_cast<SelSmem*>(smem_raw);
+  unsigned* kept_keys = reinterpret_cast<unsigned*>(smem_raw + sizeof(SelSmem));
+  const int cl = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int b = static_cast<int>(blockIdx.x) / cl;
+  const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = lane_id();
   const int raw = A.seq_len[b];
-  if (tid == 0 && (raw < 0 || raw > A.max_blocks * 64)) raise_error(A.err, kErrBounds);
   const int n = max(0, min(raw, A.max_blocks * 64));
   int* idx = A.idx + static_cast<long long>(b) * A.budget;
-  __syncthreads();
-  if (tid == 0) A.seq_len_out[b] = min(n, A.budget);
+  if (tid == 0) sm.skip = launch_aborted(A.err);
+  cluster_sync();                               // also: seq_len_out may be seq_len
+  if (ld_cluster(mapa(smem_u32(&sm.skip), 0))) {
+    cluster_sync();
+    return;
+  }
+  if (rank == 0 && tid == 0) {
+    if (raw != n) raise_error(A.err, kErrBounds);
+    A.seq_len_out[b] = min(n, A.budget);
+  }
   if (n <= A.budget) {
-    for (int i = tid; i < A.budget; i += kSelThreads) idx[i] = i < n ? i : -1;
+    for (int i = rank * kSelThreads + tid; i < A.budget; i += cl * kSelThreads)
+      idx[i] = i < n ? i : -1;
     return;
   }
   const float* mass = A.mass + b * A.ld;
-  const int lo = A.sinks, hi = n - A.recent;      // candidates
+  const int lo = A.sinks, hi = n - A.recent;    // candidates
   const int want = A.budget - A.sinks - A.recent;
-  // threshold: the want-th largest key; `ties` of the keys equal to it are kept
+  // each warp of the cluster has a run of `seg` slots, each CTA 32 such runs
+  const int warps = cl * kSelWarps;
+  const int seg = ((n + warps - 1) / warps + 31) / 32 * 32;
+  const int base = rank * kSelWarps * seg, end = min(n, base + kSelWarps * seg);
+  const bool in_smem = kSelWarps * seg <= kSelKeys;
+  auto key = [&](int i) { return in_smem ? kept_keys[i - base] : total_key(__ldg(mass + i)); };
+  if (in_smem)
+    for (int i = base + tid; i < end; i += kSelThreads) kept_keys[i - base] = total_key(mass[i]);
+  // threshold: the want-th largest key of the candidates; `ties` of the keys
+  // equal to it are kept
   unsigned thr = 0xffffffffu;
   int ties = 0;
   if (want > 0) {
-    unsigned prefix = 0, left = want;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-      for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+    unsigned prefix = 0, left = static_cast<unsigned>(want);
+#pragma unroll 1
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      for (int i = tid; i < 4 * 2048; i += kSelThreads) (&sm.hist[0][0])[i] = 0;
       __syncthreads();
-      for (int i = lo + tid; i < hi; i += kSelThreads) {
-        const unsigned k = total_key(mass[i]);
-        if (shift == 24 || (k >> (shift + 8)) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1u);
+      const int i1 = min(end, hi);
+#pragma unroll 4
+      for (int i = max(base, lo) + tid; i < i1; i += kSelThreads) {
+        const unsigned k = key(i);
+        if (pass == 0 || (k >> (shift + bits)) == prefix)
+          atomicAdd(&sm.hist[lane & 3][(k >> shift) & ((1u << bits) - 1)], 1u);
       }
       __syncthreads();
-      if (tid == 0) {
-        unsigned w = left;
-        int d = 255;
-        for (; d > 0 && hist[d] < w; --d) w -= hist[d];
-        s_prefix = (prefix << 8) | static_cast<unsigned>(d);
-        s_want = w;
+      for (int d = tid; d < 2048; d += kSelThreads)
+        sm.hist[0][d] += sm.hist[1][d] + sm.hist[2][d] + sm.hist[3][d];
+      cluster_sync();
+      // this thread's two digits, from the top: 2047 - 2 tid and the one below
+      unsigned c0 = 0, c1 = 0;
+      for (int r = 0; r < cl; ++r) {
+        const uint32_t at = mapa(smem_u32(&sm.hist[0][2046 - 2 * tid]), r);
+        c1 += ld_cluster(at);
+        c0 += ld_cluster(at + 4);
       }
+      unsigned x = c0 + c1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) sm.scan[warp] = x;
       __syncthreads();
-      prefix = s_prefix;
-      left = s_want;
-      __syncthreads();
+      unsigned above = x - (c0 + c1);
+      for (int w = 0; w < warp; ++w) above += sm.scan[w];
+      if (above < left && left <= above + c0 + c1) {
+        const bool upper = left <= above + c0;
+        sm.digit = static_cast<unsigned>(2047 - 2 * tid - (upper ? 0 : 1));
+        sm.left = left - above - (upper ? 0 : c0);
+      }
+      cluster_sync();                           // also: no CTA reads another's histogram any more
+      prefix = (prefix << bits) | sm.digit;
+      left = sm.left;
     }
     thr = prefix;
     ties = static_cast<int>(left);
+  } else {
+    __syncthreads();
   }
-  int out = 0, eq_before = 0;
-  for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-    const int i = i0 + tid;
-    bool above = false, eq = false;
-    if (i < n) {
+  // counts of the warp's run, then of everything before it
+  const int s0 = min(n, base + warp * seg), s1 = min(n, s0 + seg);
+  auto classify = [&](int i, unsigned& above, unsigned& eq) {
+    bool a = false, e = false;
+    if (i < s1) {
       if (i < lo || i >= hi) {
-        above = true;
+        a = true;
       } else if (want > 0) {
-        const unsigned k = total_key(mass[i]);
-        above = k > thr;
-        eq = k == thr;
+        const unsigned k = key(i);
+        a = k > thr;
+        e = k == thr;
       }
     }
-    int neq, nkeep;
-    const int rank = eq_before + block_prefix(eq, warp_sums, &neq);
-    const bool keep = above || (eq && rank < ties);
-    const int at = out + block_prefix(keep, warp_sums, &nkeep);
-    if (keep) idx[at] = i;
-    out += nkeep;
-    eq_before += neq;
+    above = __ballot_sync(0xffffffffu, a);
+    eq = __ballot_sync(0xffffffffu, e);
+  };
+  int n_above = 0, n_eq = 0;
+#pragma unroll 4
+  for (int i = s0; i < s1; i += 32) {
+    unsigned a, e;
+    classify(i + lane, a, e);
+    n_above += __popc(a);
+    n_eq += __popc(e);
   }
+  if (lane == 0) {
+    sm.warp_above[warp] = n_above;
+    sm.warp_eq[warp] = n_eq;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int a = 0, e = 0;
+    for (int w = 0; w < kSelWarps; ++w) {
+      a += sm.warp_above[w];
+      e += sm.warp_eq[w];
+    }
+    sm.above = a;
+    sm.eq = e;
+  }
+  cluster_sync();
+  int above_before = 0, eq_before = 0;
+  for (int r = 0; r < rank; ++r) {
+    above_before += static_cast<int>(ld_cluster(mapa(smem_u32(&sm.above), r)));
+    eq_before += static_cast<int>(ld_cluster(mapa(smem_u32(&sm.eq), r)));
+  }
+  for (int w = 0; w < warp; ++w) {
+    above_before += sm.warp_above[w];
+    eq_before += sm.warp_eq[w];
+  }
+  const unsigned below = (1u << lane) - 1;
+#pragma unroll 2
+  for (int i = s0; i < s1; i += 32) {
+    unsigned a, e;
+    classify(i + lane, a, e);
+    const int ra = above_before + __popc(a & below), re = eq_before + __popc(e & below);
+    if (((a >> lane) & 1u) || (((e >> lane) & 1u) && re < ties)) idx[ra + min(ties, re)] = i + lane;
+    above_before += __popc(a);
+    eq_before += __popc(e);
+  }
+  cluster_sync();                               // the others may still read this CTA's counts
 }
 
-// One column slice of one sequence: `width` bytes of every row of a pool
-// (rows of `pitch` bytes), kMoveThreads / (width / 4) rows a step.
+// One column slice of one sequence: `cols` elements from element `first` of
+// every row (rows of `pitch` elements), kMoveRows * threads / cols rows a step.
+// The next step's rows are on their way while a step's are written.
 template <typename V>
-__device__ __forceinline__ void move_columns(const EvictArgs& A, int b, int count, V* pool,
-                                             int pitch_v, int cols_v, int first_v) {
-  const int rows = kMoveThreads / cols_v;
-  const int col = static_cast<int>(threadIdx.x) % cols_v, sub = static_cast<int>(threadIdx.x) / cols_v;
+__device__ __forceinline__ void move_columns(const EvictArgs& A, int b, int count, const V* from,
+                                             V* to, bool paged, int pitch, int cols, int first) {
+  const int per = kMoveThreads / cols;          // rows of one sub-step
+  const int col = first + static_cast<int>(threadIdx.x) % cols;
+  const int sub = static_cast<int>(threadIdx.x) / cols;
   const int* idx = A.idx + static_cast<long long>(b) * A.budget;
   const int* table = A.block_table + static_cast<long long>(b) * A.max_blocks;
   auto row = [&](int s) -> long long {
-    const int pb = table[s >> 6];
+    if (!paged) return s;
+    const int pb = __ldg(table + (s >> 6));
     return pb < 0 || pb >= A.nblk ? -1 : static_cast<long long>(pb) * 64 + (s & 63);
   };
-  for (int j0 = 0; j0 < count; j0 += rows) {
-    const int j = j0 + sub;
-    V v = {};
-    long long to = -1;
-    if (sub < rows && j < count && idx[j] != j) {
-      const long long from = row(idx[j]);
-      to = row(j);
-      if (from < 0 || to < 0) {
-        raise_error(A.err, kErrBounds);
-        to = -1;
-      } else {
-        v = pool[from * pitch_v + first_v + col];
-      }
+  V v[2][kMoveRows];
+  int src[kMoveRows];
+  auto slots = [&](int j0) {
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const int j = j0 + u * per + sub;
+      src[u] = j < count ? __ldg(idx + j) : -1;
     }
-    __syncthreads();
-    if (to >= 0) pool[to * pitch_v + first_v + col] = v;
+  };
+  auto load = [&](int j0, V (&w)[kMoveRows]) {
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const int j = j0 + u * per + sub;
+      if (src[u] < 0 || (src[u] == j && from == to)) continue;
+      const long long r = row(src[u]);
+      if (r >= 0) w[u] = from[r * pitch + col];
+    }
+  };
+  const int step = kMoveRows * per;
+  slots(0);
+  load(0, v[0]);
+  int ph = 0;
+  for (int j0 = 0; j0 < count; j0 += step, ph ^= 1) {
+    int at[kMoveRows];
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) at[u] = src[u];
+    slots(j0 + step);
+    if (ph == 0)
+      load(j0 + step, v[1]);
+    else
+      load(j0 + step, v[0]);
+    __syncthreads();                            // the step's rows are read
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const int j = j0 + u * per + sub;
+      if (at[u] < 0 || (at[u] == j && from == to)) continue;
+      const long long r = row(j);
+      if (r < 0 || row(at[u]) < 0)
+        raise_error(A.err, kErrBounds);
+      else
+        to[r * pitch + col] = ph == 0 ? v[0][u] : v[1][u];
+    }
   }
 }
 
-constexpr int kKvSlices = 9;       // 128 bytes of the latent row each
-
+// kCols: 16-byte columns of a slice (divides 8 and 72).
+template <int kCols>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs A) {
   const int b = static_cast<int>(blockIdx.y);
-  const int slice = static_cast<int>(blockIdx.x);
+  if (__syncthreads_or(launch_aborted(A.err))) return;
   const int count = A.seq_len_out[b];
-  if (slice < kKvSlices) {
-    move_columns(A, b, count, static_cast<uint4*>(A.kv_pool), 72, 8, 8 * slice);
-  } else if (slice == kKvSlices) {
-    if (A.k8_pool) move_columns(A, b, count, static_cast<uint4*>(A.k8_pool), 8, 8, 0);
-  } else if (slice == kKvSlices + 1) {
-    if (A.k_scale_pool) move_columns(A, b, count, A.k_scale_pool, 1, 1, 0);
+  constexpr int kKv = 72 / kCols, kK8 = 8 / kCols;
+  int s = static_cast<int>(blockIdx.x);
+  if (s < kKv) {
+    uint4* p = static_cast<uint4*>(A.kv_pool);
+    move_columns<uint4>(A, b, count, p, p, true, 72, kCols, kCols * s);
+  } else if ((s -= kKv) < kK8) {
+    uint4* p = static_cast<uint4*>(A.k8_pool);
+    if (p) move_columns<uint4>(A, b, count, p, p, true, 8, kCols, kCols * s);
+  } else if (s == kK8) {
+    if (A.k_scale_pool)
+      move_columns<float>(A, b, count, A.k_scale_pool, A.k_scale_pool, true, 1, 1, 0);
   } else if (A.mass_out) {
-    const int* idx = A.idx + static_cast<long long>(b) * A.budget;
-    for (int j0 = 0; j0 < count; j0 += kMoveThreads) {
-      const int j = j0 + static_cast<int>(threadIdx.x);
-      const float v = j < count ? A.mass[b * A.ld + idx[j]] : 0.f;
-      __syncthreads();
-      if (j < count) A.mass_out[b * A.ld_out + j] = v;
-    }
+    move_columns<float>(A, b, count, A.mass + b * A.ld, A.mass_out + b * A.ld_out, false, 1, 1, 0);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st) {
-  evict_select_kernel<<<a.B, kSelThreads, 0, st>>>(a);
-  cudaError_t e = cudaGetLastError();
+  // CTAs per sequence: more while they leave SMs idle and have 4096 slots each
+  int cl = 1;
+  while (cl < 8 && a.B * cl * 2 <= 148 && a.max_blocks * 64 > 4096 * cl) cl *= 2;
+  const size_t smem = sizeof(SelSmem) + kSelKeys * sizeof(unsigned);
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  evict_move_kernel<<<dim3(kKvSlices + 3, a.B), kMoveThreads, 0, st>>>(a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B) * cl);
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = static_cast<unsigned>(cl);
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+  if (e != cudaSuccess) return e;
+  // Slices as wide as leaves two CTAs an SM: 128-byte columns move whole lines,
+  // 16-byte ones give a single sequence 82 CTAs.
+  const int want = 2 * 148;
+  if (a.B * 12 >= want)
+    evict_move_kernel<8><<<dim3(12, a.B), kMoveThreads, 0, st>>>(a);
+  else if (a.B * 22 >= want)
+    evict_move_kernel<4><<<dim3(22, a.B), kMoveThreads, 0, st>>>(a);
+  else if (a.B * 42 >= want)
+    evict_move_kernel<2><<<dim3(42, a.B), kMoveThreads, 0, st>>>(a);
+  else
+    evict_move_kernel<1><<<dim3(82, a.B), kMoveThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
