@@ -98,7 +98,8 @@ struct Ctl {
   unsigned long long v_full[kVRing], v_empty[kVRing];
   unsigned long long p_full[kPSlots], p_free[kPSlots];
   unsigned long long al_full[4];                // a tile's rescale factors have landed
-  unsigned long long o_ok[4];                   // O and V are ready for a tile's PV
+  unsigned long long o_ok[4];                   // O is ready for a tile's PV
+  unsigned long long clean[2];                  // V of a tile's unit with hidden keys is ready
   unsigned long long pv_done[4];
   unsigned long long o_done;
   unsigned long long ml_full;
@@ -108,6 +109,14 @@ struct Ctl {
 };
 constexpr size_t kSmemBytes = kBig + sizeof(Ctl) + 1024;
 static_assert(kSmemBytes <= 232448, "fits the 227 KB of shared memory a CTA may use");
+
+// The bits a .. b of 0 .. 63 (none if a > b).
+__device__ __forceinline__ unsigned long long range_bits(int a, int b) {
+  a = max(a, 0);
+  b = min(b, 63);
+  if (a > b) return 0ull;
+  return (~0ull >> (63 - b)) & (~0ull << a);
+}
 
 // A row tile: its rows, positions and 64-key units.
 struct Item {
@@ -169,6 +178,15 @@ __device__ __forceinline__ int unit_block(const Item& x, int u) {
 }
 __device__ __forceinline__ int tile_units(const Item& x, int t) {
   return x.nu - 2 * t >= 2 ? 2 : 1;
+}
+// The keys of unit u (bits) that some query of the row tile does not see, though
+// they are loaded: past the first query's position, or before the last query's
+// window (and no sink).
+__device__ __forceinline__ unsigned long long unit_hidden(const RangeArgs& A, const Item& x, int u) {
+  const int kb = unit_block(x, u) * 64;
+  unsigned long long hidden = range_bits(min(x.pos0, x.last) + 1 - kb, 63);
+  if (A.window) hidden |= range_bits(A.sinks - kb, x.posl - A.window - kb);
+  return hidden;
 }
 // Cache row of unit u's first key, or kv_rows (whose loads give zeros) when
 // the row tile has no keys or the block id is out of range.
@@ -233,15 +251,6 @@ struct Walk {
     return more;
   }
 };
-
-// Bits of the 64 keys from kb on that a row with positions [lo, hi] and the
-// first `sinks` keys sees.
-__device__ __forceinline__ unsigned long long range_bits(int a, int b) {
-  a = max(a, 0);
-  b = min(b, 63);
-  if (a > b) return 0ull;
-  return (~0ull >> (63 - b)) & (~0ull << a);
-}
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -316,6 +325,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     init(ctl.ml_free, 8);
     init(ctl.o_done, 1);
+    init(ctl.clean[0], 8);
+    init(ctl.clean[1], 8);
     init(ctl.ml_full, 8);
     ctl.abort_flag = launch_aborted(err) ? 1 : 0;
     fence_barrier_init();
@@ -729,6 +740,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const uint64_t p_d = sdesc_sw128(smem_u32(so.p[0]), 0, 1024);
       const uint64_t v_d = sdesc_sw128(smem_u32(so.v[0]), kUnitAtom, 1024);
       int vc = 0, tc = 0, ac = 0;
+      unsigned cleaned = 0;                             // parity of each unit's uses of `clean`
       while (ok && walk.next(A, p, x)) {
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
           const int n = tile_units(x, t);
@@ -737,6 +749,10 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           for (int u = 0; ok && u < n; ++u, ++ac) {
             const int slot = ac & 3;
             if (!(ok = wait32<true>(ctl.p_full[slot], (ac >> 2) & 1, abort_flag, err))) break;
+            if (2 * t + u < x.nu && unit_hidden(A, x, 2 * t + u) != 0ull) {
+              if (!(ok = wait32(ctl.clean[u], (cleaned >> u) & 1, abort_flag, err))) break;
+              cleaned ^= 1u << u;
+            }
             const uint64_t pd = p_d + slot * (kAtom >> 4);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h, ++vc) {
@@ -806,34 +822,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
           const int n = tile_units(x, t);
           const int sl4 = tc & 3;
-          // a tile some row does not see whole: its P holds zeros, and a zero
-          // times a NaN or infinite value would reach that row
-          bool edge = false;
-          for (int u = 2 * t; u < min(2 * t + n, x.nu); ++u) {
-            const int kb = unit_block(x, u) * 64;
-            edge |= kb + 63 > min(x.pos0, x.last) ||
-                    (A.window && kb < x.posl - A.window + 1 && kb + 63 >= A.sinks);
-          }
-          // (every tile's chunks are waited for, so that no phase is missed)
-          for (int c = vc; ok && c < vc + 2 * n; ++c) {
-            if (!(ok = wait32(ctl.v_full[c & 3], (c >> 2) & 1, abort_flag, err))) break;
-            if (edge) {
-              uint4* v = reinterpret_cast<uint4*>(so.v[c & 3]);
-              auto clean = [](uint32_t w) {
-                if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-                if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-                return w;
-              };
-              for (int i = threadIdx.x - 128; i < kVChunk / 16; i += 256) {
-                const uint4 o = v[i];
-                const uint4 w = make_uint4(clean(o.x), clean(o.y), clean(o.z), clean(o.w));
-                if (w.x != o.x || w.y != o.y || w.z != o.z || w.w != o.w) v[i] = w;
-              }
-            }
-          }
-          if (!ok) break;
-          if (edge) fence_proxy_async_smem();
-          vc += 2 * n;
           if (!(ok = wait32<true>(ctl.al_full[sl4], (tc >> 2) & 1, abort_flag, err))) break;
           if (threadIdx.x == 128) mbar_expect_tx(smem_u32(&ctl.al_full[sl4]), 512);
           const float alpha = so.alpha[sl4][r];
@@ -854,6 +842,46 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl.o_ok[sl4]));
+          // Keys that some row does not see have zeros in its P, and a zero
+          // times a NaN or infinite value would reach that row: such values
+          // become 0 (a row that sees them has a NaN logit). PV of this unit
+          // waits for `clean`.
+          for (int u = 0; u < n; ++u, vc += 2) {
+            const unsigned long long hidden =
+                2 * t + u < x.nu ? unit_hidden(A, x, 2 * t + u) : 0ull;
+            if (hidden == 0ull) continue;
+            // once the tile before is done, its chunks' barriers are in the
+            // phase before the one waited for
+            if (t > p.t0 && !(ok = wait32(ctl.pv_done[(tc + 3) & 3], ((tc - 1) >> 2) & 1,
+                                          abort_flag, err)))
+              break;
+            const int k0 = __ffsll(static_cast<long long>(hidden)) - 1;
+            const int k1 = 64 - __clzll(static_cast<long long>(hidden));
+            for (int h = 0; h < 2; ++h) {
+              const int c = vc + h;
+              if (!(ok = wait32(ctl.v_full[c & 3], (c >> 2) & 1, abort_flag, err))) break;
+              auto clean = [](uint32_t w) {
+                if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+                if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
+                return w;
+              };
+              // rows k0 .. k1 - 1 of the chunk's four atoms, 8 x 16 B each
+              uint8_t* v = so.v[c & 3];
+              const int sub = static_cast<int>(threadIdx.x) - 128;
+#pragma unroll 2
+              for (int i = sub >> 3; i < 4 * (k1 - k0); i += 32) {
+                uint4* at = reinterpret_cast<uint4*>(v + (i & 3) * kUnitAtom +
+                                                     (k0 + (i >> 2)) * 128 + (sub & 7) * 16);
+                const uint4 o = *at;
+                const uint4 w = make_uint4(clean(o.x), clean(o.y), clean(o.z), clean(o.w));
+                if (w.x != o.x || w.y != o.y || w.z != o.z || w.w != o.w) *at = w;
+              }
+            }
+            if (!ok) break;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.clean[u]));
+          }
         }
         if (!ok) break;
         // ------------------------------------------------------- a piece's end
