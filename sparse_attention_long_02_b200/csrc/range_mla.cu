@@ -818,7 +818,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const uint32_t o_cols = tmem + (static_cast<uint32_t>(32 * wq) << 16) + 256 * g;
       int tc = 0, vc = 0, pieces = 0;
       bool recorded = false;
-      while (ok && walk.next(A, p, x)) {
+      bool more = ok && walk.next(A, p, x);
+      while (ok && more) {
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
           const int n = tile_units(x, t);
           const int sl4 = tc & 3;
@@ -894,6 +895,10 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         (a1.x > -INFINITY ? a1.y * fast_exp2(a1.x - m) : a1.y);
         if (!(ok = wait32(ctl.o_done, pieces & 1, abort_flag, err))) break;
         tc_fence_after();
+        // the next piece is worked out before this one's stores fill the queues
+        Piece p_next;
+        Item x_next;
+        more = walk.next(A, p_next, x_next);
         const bool valid = r < x.nrows;
         if (p.first && p.last) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -959,6 +964,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
         ++pieces;
+        p = p_next;
+        x = x_next;
       }
       if (threadIdx.x == 128 && !recorded && A.rec) A.rec[cluster] = make_int2(-1, 0);
     }
