@@ -19,8 +19,8 @@
 //   CTA 0: Q's 512 latent dims move into TMEM (256 columns; the rope dims stay
 //     in shared memory), K chunks (128 keys x 64 dims) stream through a ring of
 //     TMA loads; S = Q K^T (M = 128, N = 128, K = 576) goes into one of two
-//     TMEM buffers; two groups of four warps (thread = row) take the tiles in
-//     turn: row maximum, running reference maximum (re-based only when it
+//     TMEM buffers; two groups of four warps (thread = row) take 64 keys of a
+//     tile each: row maximum, running reference maximum (re-based only when it
 //     grows by more than 8 in log2 units), P = exp2(z - m) in bf16 into shared
 //     memory, one 16 KB bulk copy per 64 keys into CTA 1.
 //   CTA 1: V chunks (64 keys x 256 dims) stream through their own ring;
@@ -57,7 +57,7 @@ constexpr int kQPairs = 4;                      // Q dims [0, 512) live in TMEM,
 constexpr uint32_t kColQ = 256;                 // after two buffers of 128 logits
 constexpr int kPSlots = 4;
 constexpr int kVRing = 4;
-constexpr int kAhead = 6;                       // tiles of L2 prefetch, ahead of CTA 1
+constexpr int kAhead = 3;                       // tiles of L2 prefetch, ahead of CTA 1's V
 constexpr float kRebase = 8.0f;                 // lazy rescale threshold (log2 units)
 constexpr int kMaxClusters = 74;                // two CTAs on each of 148 SMs
 constexpr int kScanItems = 16384;               // row tiles a cluster scans for its share
@@ -66,16 +66,16 @@ constexpr int kMinShare = 2;                    // tiles (and fixed costs) a clu
 
 struct LogitsSmem {                             // CTA 0
   uint8_t ring[kRing][kEntry];                  // K, and Q on its way to TMEM
-  uint8_t p[2][2][kAtom];                       // staging of P, by softmax group and unit
+  uint8_t p[2][2][kAtom];                       // staging of P, by tile parity and unit
   uint8_t q_rope[kAtom];                        // Q dims [512, 576)
-  float alpha[2][128];                          // staging of the rescale factors, by group
-  float m[2][128];                              // reference maxima, by tile parity
+  float alpha[2][128];                          // staging of the rescale factors, by tile parity
+  float mx[2][2][128];                          // maxima, by tile parity and softmax group
 };
 struct OutputSmem {                             // CTA 1
   uint8_t p[kPSlots][kAtom];
   uint8_t v[kVRing][kVChunk];
   float alpha[4][128];                          // rescale factors, by tile
-  float2 ml[2][128];                            // maximum and sum of each softmax group
+  float2 ml[2][128];                            // reference maximum and sum of each softmax group
   uint8_t stage[8][32 * 64];                    // output rows on their way out, by warp
 };
 constexpr size_t kBig = std::max(sizeof(LogitsSmem), sizeof(OutputSmem));
@@ -87,9 +87,9 @@ struct Ctl {
   unsigned long long q_ready[kQPairs];          // 128 dims of Q are in TMEM
   unsigned long long rope_full;
   unsigned long long k_full[kRing], k_empty[kRing];
-  unsigned long long s_full[2], s_empty[2];     // by softmax group
-  unsigned long long m_bar[4];                  // a tile's reference maxima of a lane quarter
-  // by softmax group and unit, so that whoever waits on one sees every phase
+  unsigned long long s_full[2], s_empty[2];     // by tile parity
+  unsigned long long mx_bar[4];                 // both groups' maxima of a lane quarter
+  // by tile parity and unit, so that whoever waits on one sees every phase
   unsigned long long p_own[2][2];               // a staged atom is written
   unsigned long long p_ack[2][2];               // CTA 1 holds the atom: its staging is free
   unsigned long long p_room[kPSlots];           // CTA 1 has room for another atom
@@ -104,6 +104,7 @@ struct Ctl {
   unsigned long long o_done;
   unsigned long long ml_full;
   Share share;                                  // of the row tiles' weights
+  int progress;                                 // CTA 1: tiles whose V loads have begun
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -189,13 +190,17 @@ __device__ __forceinline__ unsigned long long unit_hidden(const RangeArgs& A, co
   return hidden;
 }
 // Cache row of unit u's first key, or kv_rows (whose loads give zeros) when
-// the row tile has no keys or the block id is out of range.
-__device__ __forceinline__ int unit_row(const RangeArgs& A, const Item& x, int u) {
-  if (u >= x.nu) return A.kv_rows;
+// the row tile has no keys or the block id is out of range. In two steps, so
+// that a tile's table entries can be on their way while the tile before is
+// loaded.
+__device__ __forceinline__ int unit_entry(const RangeArgs& A, const Item& x, int u) {
+  if (u >= x.nu) return -1;
   const int block = unit_block(x, u);
-  if (!A.block_table) return block * 64;
-  const int pb = __ldg(x.table + block);
-  return pb < 0 || pb >= A.nblk ? A.kv_rows : pb * 64;
+  return A.block_table ? __ldg(x.table + block) : block;
+}
+__device__ __forceinline__ int entry_row(const RangeArgs& A, int entry) {
+  const bool bad = entry < 0 || (A.block_table && entry >= A.nblk);
+  return bad ? A.kv_rows : entry * 64;
 }
 
 // A cluster's share, one piece (tiles [t0, t1) of a row tile) after another.
@@ -307,7 +312,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       init(ctl.q_ready[i], 4);
       init(ctl.k_full[i], 1);
       init(ctl.k_empty[i], 1);
-      init(ctl.m_bar[i], 1);
+      init(ctl.mx_bar[i], 2);
       init(ctl.p_own[i >> 1][i & 1], 4);
       init(ctl.p_ack[i >> 1][i & 1], 1);
       init(ctl.p_room[i], 1);
@@ -321,7 +326,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     for (int i = 0; i < 2; ++i) {
       init(ctl.s_full[i], 1);
-      init(ctl.s_empty[i], 4);
+      init(ctl.s_empty[i], 8);
     }
     init(ctl.ml_free, 8);
     init(ctl.o_done, 1);
@@ -329,6 +334,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     init(ctl.clean[1], 8);
     init(ctl.ml_full, 8);
     ctl.abort_flag = launch_aborted(err) ? 1 : 0;
+    ctl.progress = 0;
     fence_barrier_init();
     // CTA 1 expects the first atoms of P before CTA 0 can send one
     if (rank == 1)
@@ -364,12 +370,12 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         int ent = 0, pieces = 0;
         while (ok && walk.next(A, p, x)) {
           const int q_row = static_cast<int>(x.row0);
-          int r0 = unit_row(A, x, 2 * p.t0), r1 = unit_row(A, x, 2 * p.t0 + 1);
+          int e0 = unit_entry(A, x, 2 * p.t0), e1 = unit_entry(A, x, 2 * p.t0 + 1);
           for (int t = p.t0; ok && t < p.t1; ++t) {
             const int n = tile_units(x, t);
-            const int c0 = r0, c1 = r1;
-            r0 = unit_row(A, x, 2 * t + 2);
-            r1 = unit_row(A, x, 2 * t + 3);
+            const int c0 = entry_row(A, e0), c1 = entry_row(A, e1);
+            e0 = unit_entry(A, x, 2 * t + 2);
+            e1 = unit_entry(A, x, 2 * t + 3);
             const bool with_q = t == p.t0;
             const int count = with_q ? 5 + kQPairs : 5;
 #pragma unroll 1
@@ -560,10 +566,16 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
     } else {
       // -------------------------------------------------- softmax (CTA 0)
-      const int g = (warp - 4) >> 2;                    // takes the tiles of its parity
+      // Thread = row; group g takes unit g of every tile. P is formed at once
+      // with the reference maximum of the tile before, while the tile's own
+      // maximum is found; the two groups then swap maxima, and only where the
+      // reference has to move is P formed again. (A piece's first tile looks
+      // for its maximum first.)
+      const int g = (warp - 4) >> 2;
       const int wq = warp & 3;                          // TMEM lane quarter
       const int r = 32 * wq + lane;                     // row = TMEM lane
       const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
+      const float2 scale2 = make_float2(A.sm_scale_log2, A.sm_scale_log2);
       int tc = 0, pieces = 0;
       unsigned acked = 3u;                              // parity of each staging's uses, before the first
       while (ok && walk.next(A, p, x)) {
@@ -571,120 +583,114 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const int hi = r < x.nrows ? min(pos, x.last) : -1;
         const int lo = A.window ? pos - A.window + 1 : 0;
         const int sink_hi = A.window ? min(A.sinks - 1, hi) : -1;
-        float m_own = -INFINITY, l = 0.f;
-        for (int t = p.t0; ok && t < p.t1; ++t) {
-          const int n = tile_units(x, t);
-          if ((tc & 1) == g) {
-            unsigned long long vis0 = 0ull, vis1 = 0ull;
-            for (int un = 2 * t; un < min(2 * t + 2, x.nu); ++un) {
-              const int block = unit_block(x, un);
-              bool good = true;
-              if (A.block_table) {
-                const int pb = __ldg(x.table + block);
-                good = pb >= 0 && pb < A.nblk;
-                if (!good && lane == 0) raise_error(err, kErrBounds);
-              }
-              const int kb = block * 64;
-              const unsigned long long see =
-                  good ? range_bits(lo - kb, hi - kb) | range_bits(0, sink_hi - kb) : 0ull;
-              if (un & 1)
-                vis1 = see;
-              else
-                vis0 = see;
+        float m = -INFINITY, l = 0.f;
+        for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
+          const int n = tile_units(x, t), b = tc & 1, un = 2 * t + g;
+          unsigned long long see = 0ull;                // keys of the unit that the row sees
+          if (un < x.nu) {
+            const int block = unit_block(x, un);
+            bool good = true;
+            if (A.block_table) {
+              const int pb = __ldg(x.table + block);
+              good = pb >= 0 && pb < A.nblk;
+              if (!good && lane == 0) raise_error(err, kErrBounds);
             }
-            if (!(ok = wait32(ctl.s_full[g], (tc >> 1) & 1, abort_flag, err))) break;
-            tc_fence_after();
-            const uint32_t s_cols = tmem + lanes + 128 * g;
-            float mx = -INFINITY;
+            const int kb = block * 64;
+            if (good) see = range_bits(lo - kb, hi - kb) | range_bits(0, sink_hi - kb);
+          }
+          const uint32_t s_cols = tmem + lanes + 128 * b + 64 * g;
+          const bool first = t == p.t0;
+          uint8_t* row = sl.p[b][g] + r * 128;
+          float mx = -INFINITY;
+          float2 sum2;
+          // P = exp2(z - base) of the unit into the staging, its sum, and the
+          // unit's maximum of the raw logits
+          auto form = [&](float base) {
+            const float2 base2 = make_float2(-base, -base);
+            sum2 = make_float2(0.f, 0.f);
 #pragma unroll 1
-            for (int u = 0; u < n; ++u) {
-              float s[64];
-              tmem_ld64(s_cols + 64 * u, s);
-              const unsigned long long see = u ? vis1 : vis0;
-              if (!__all_sync(0xffffffffu, see == ~0ull)) {
+            for (int h = 0; h < 2; ++h) {
+              float s[32];
+              tmem_ld32(s_cols + 32 * h, s);
+              const unsigned bits = static_cast<unsigned>(see >> (32 * h));
+              if (!__all_sync(0xffffffffu, bits == ~0u)) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                  if (!((see >> e) & 1ull)) s[e] = -INFINITY;
+                for (int e = 0; e < 32; ++e)
+                  if (!((bits >> e) & 1u)) s[e] = -INFINITY;
               }
               float pm[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-              for (int e = 0; e < 64; ++e) pm[e & 3] = fmaxf(pm[e & 3], s[e]);
+              for (int e = 0; e < 32; ++e) pm[e & 3] = fmaxf(pm[e & 3], s[e]);
               mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+              // row r of the atom: 128 B, 16-B chunk c at chunk c ^ (r % 8)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                uint32_t pk[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  float2 v =
+                      fma2(make_float2(s[8 * c + 2 * e], s[8 * c + 2 * e + 1]), scale2, base2);
+                  v.x = fast_exp2(v.x);
+                  v.y = fast_exp2(v.y);
+                  sum2 = add2(sum2, v);
+                  const __nv_bfloat162 pb = __floats2bfloat162_rn(v.x, v.y);
+                  pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
+                }
+                *reinterpret_cast<uint4*>(row + (((4 * h + c) ^ (r & 7)) << 4)) =
+                    make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              }
             }
-            mx *= A.sm_scale_log2;
-            // the other group's reference maximum of the tile before
-            if (tc > 0 && !(ok = wait32(ctl.m_bar[wq], (tc - 1) & 1, abort_flag, err))) break;
-            const bool first = t == p.t0;
-            const float m_prev = first ? -INFINITY : sl.m[(tc + 1) & 1][r];
-            const float m_new = mx > m_prev + kRebase ? mx : m_prev;
-            sl.m[tc & 1][r] = m_new;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl.m_bar[wq]));
-            const bool re = m_prev > -INFINITY && m_new != m_prev;
-            if (m_own > -INFINITY && m_own != m_new) l *= fast_exp2(m_own - m_new);
-            m_own = m_new;
-            const float base = m_new == -INFINITY ? 0.f : m_new;
-            const float2 scale2 = make_float2(A.sm_scale_log2, A.sm_scale_log2);
-            const float2 base2 = make_float2(-base, -base);
-            float2 sum2 = make_float2(0.f, 0.f);
-#pragma unroll 1
-            for (int u = 0; u < n; ++u) {
-              // the staging is free once CTA 1 holds what it held (a barrier not
-              // yet used passes for the phase before its first)
-              if (!(ok = wait32<true>(ctl.p_ack[g][u], (acked >> u) & 1, abort_flag, err))) break;
-              acked ^= 1u << u;
-              if (u == 0) sl.alpha[g][r] = re ? fast_exp2(m_prev - m_new) : 1.f;
-              uint8_t* row = sl.p[g][u] + r * 128;
+          };
+          // the staging is free once CTA 1 holds what it held (a barrier not
+          // yet used passes for the phase before its first)
+          if (g < n) {
+            if (!(ok = wait32<true>(ctl.p_ack[b][g], (acked >> b) & 1, abort_flag, err))) break;
+            acked ^= 1u << b;
+          }
+          if (!(ok = wait32(ctl.s_full[b], (tc >> 1) & 1, abort_flag, err))) break;
+          tc_fence_after();
+          if (g < n) {
+            if (first) {
 #pragma unroll 1
               for (int h = 0; h < 2; ++h) {
                 float s[32];
-                tmem_ld32(s_cols + 64 * u + 32 * h, s);
-                const unsigned bits = static_cast<unsigned>((u ? vis1 : vis0) >> (32 * h));
+                tmem_ld32(s_cols + 32 * h, s);
+                const unsigned bits = static_cast<unsigned>(see >> (32 * h));
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  const float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), scale2, base2);
-                  s[2 * e] = fast_exp2(z.x);
-                  s[2 * e + 1] = fast_exp2(z.y);
-                }
-                if (!__all_sync(0xffffffffu, bits == ~0u)) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (!((bits >> e) & 1u)) s[e] = 0.f;
-                }
-                // row r of the atom: 128 B, 16-B chunk c at chunk c ^ (r % 8)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  uint32_t pk[4];
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) {
-                    const float2 v = make_float2(s[8 * c + 2 * e], s[8 * c + 2 * e + 1]);
-                    sum2 = add2(sum2, v);
-                    const __nv_bfloat162 pb = __floats2bfloat162_rn(v.x, v.y);
-                    pk[e] = *reinterpret_cast<const uint32_t*>(&pb);
-                  }
-                  *reinterpret_cast<uint4*>(row + (((4 * h + c) ^ (r & 7)) << 4)) =
-                      make_uint4(pk[0], pk[1], pk[2], pk[3]);
-                }
+                for (int e = 0; e < 32; ++e) mx = fmaxf(mx, (bits >> e) & 1u ? s[e] : -INFINITY);
               }
-              if (u + 1 == n) {                         // the buffer is free for another tile
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&ctl.s_empty[g]));
-              }
-              fence_proxy_async_smem();                 // generic writes -> bulk-copy reads
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&ctl.p_own[g][u]));
+            } else {
+              form(m == -INFINITY ? 0.f : m);
             }
-            l += sum2.x + sum2.y;
           }
-          ++tc;
+          // the row's maximum over both units
+          sl.mx[b][g][r] = mx;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl.mx_bar[wq]));
+          if (!(ok = wait32(ctl.mx_bar[wq], tc & 1, abort_flag, err))) break;
+          const float top = fmaxf(mx, sl.mx[b][g ^ 1][r]) * A.sm_scale_log2;
+          const float m_new = top > m + kRebase ? top : m;
+          const bool moved = m_new != m;
+          const float alpha = moved && m > -INFINITY ? fast_exp2(m - m_new) : 1.f;
+          m = m_new;
+          if (g < n && (first || __any_sync(0xffffffffu, moved)))
+            form(m == -INFINITY ? 0.f : m);
+          if (g == 0) sl.alpha[b][r] = alpha;
+          l = g < n ? l * alpha + (sum2.x + sum2.y) : l * alpha;
+          fence_proxy_async_smem();                     // generic writes -> bulk-copy reads
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(smem_u32(&ctl.s_empty[b]));     // the buffer is free for another tile
+            if (g < n) mbar_arrive(smem_u32(&ctl.p_own[b][g]));
+          }
         }
         if (!ok) break;
         // the group's maximum and sum go to CTA 1
         if (pieces > 0 && !(ok = wait32<true>(ctl.ml_free, (pieces - 1) & 1, abort_flag, err)))
           break;
         const uint32_t ml = mapa(smem_u32(&so.ml[g][r]), peer);
-        st_cluster_f32(ml, m_own);
+        st_cluster_f32(ml, m);
         st_cluster_f32(ml + 4, l);
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctl.ml_full), peer));
@@ -696,29 +702,16 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // ---------------------------------------------------- V loads (CTA 1)
       if (lane == 0) {
         int vc = 0;
-        // brings a unit into L2 (row kv_rows: none)
-        auto prefetch = [&](int row) {
-          if (row < A.kv_rows)
-            prefetch_l2(A.kv + static_cast<long long>(row) * 576,
-                        1152u * static_cast<unsigned>(min(64, A.kv_rows - row)));
-        };
+        volatile int* progress = &ctl.progress;
+        int tc = 0;
         while (ok && walk.next(A, p, x)) {
-          for (int u = 2 * p.t0 + 2; u < min(2 * (p.t0 + kAhead), 2 * p.t1); ++u)
-            prefetch(unit_row(A, x, u));
-          // table entries are loaded a tile before they are used
-          const int u_end = min(2 * p.t1, x.nu);
-          auto ahead = [&](int u) { return u < u_end ? unit_row(A, x, u) : A.kv_rows; };
-          int r0 = unit_row(A, x, 2 * p.t0), r1 = unit_row(A, x, 2 * p.t0 + 1);
-          int f0 = ahead(2 * (p.t0 + kAhead)), f1 = ahead(2 * (p.t0 + kAhead) + 1);
+          int e0 = unit_entry(A, x, 2 * p.t0), e1 = unit_entry(A, x, 2 * p.t0 + 1);
           for (int t = p.t0; ok && t < p.t1; ++t) {
             const int n = tile_units(x, t);
-            const int c0 = r0, c1 = r1, d0 = f0, d1 = f1;
-            r0 = unit_row(A, x, 2 * t + 2);
-            r1 = unit_row(A, x, 2 * t + 3);
-            f0 = ahead(2 * (t + 1 + kAhead));
-            f1 = ahead(2 * (t + 1 + kAhead) + 1);
-            prefetch(d0);
-            prefetch(d1);
+            const int c0 = entry_row(A, e0), c1 = entry_row(A, e1);
+            e0 = unit_entry(A, x, 2 * t + 2);
+            e1 = unit_entry(A, x, 2 * t + 3);
+            *progress = ++tc;
             for (int h = 0; h < 2 * n; ++h, ++vc) {
               const int st = vc & 3;
               if (vc >= kVRing &&
@@ -807,6 +800,31 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mbar_arrive_remote(mapa(smem_u32(&ctl.p_room[slot]), peer));
               }
             }
+          }
+        }
+      }
+    } else if (warp == 12) {
+      // ------------------------------------------- L2 prefetch (CTA 1)
+      // A tile's cache lines are asked for kAhead tiles before CTA 1 loads its
+      // V (CTA 0 is about two tiles ahead of that). One warp's plain prefetches:
+      // bulk ones go through the TMA engine, whose time CTA 1 needs for V
+      // (64 x 32768: 731 us with them, 635 us with none).
+      volatile int* progress = &ctl.progress;
+      int tc = 0;
+      while (ok && walk.next(A, p, x)) {
+        for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
+          const unsigned long long t0 = globaltimer();
+          while (*progress + kAhead < tc && ok) {
+            ok = *abort_flag == 0 && globaltimer() - t0 < kWaitLimitNs;
+            __nanosleep(200);
+          }
+          ok = __all_sync(0xffffffffu, ok);
+          for (int u = 2 * t; u < min(2 * t + 2, x.nu); ++u) {
+            const int row = entry_row(A, unit_entry(A, x, u));
+            const int lines = 9 * min(64, A.kv_rows - row);     // of 128 bytes (none: row kv_rows)
+            const char* at = reinterpret_cast<const char*>(A.kv + static_cast<long long>(row) * 576);
+            for (int i = lane; i < lines; i += 32)
+              asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * i));
           }
         }
       }

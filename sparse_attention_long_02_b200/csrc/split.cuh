@@ -9,9 +9,29 @@ namespace dsa {
 // The bounded waits of common.cuh with the slow path out of line: these kernels
 // have some thirty of them in warps that run different code, and their short
 // loops have to fit the instruction caches.
-static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                       unsigned* err) {
-  return mbar_wait<true>(bar, parity, abort_flag, err);
+//
+// The slow path suspends the warp in the barrier unit, at most a millisecond at
+// a time, and spends no issue slots that the SM's other warps could use.
+static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity,
+                                              volatile int* abort_flag, unsigned* err) {
+  const unsigned long long t0 = globaltimer();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort_flag) return false;
+    if (globaltimer() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      raise_error(err, kErrTimeout);
+      return false;
+    }
+  }
 }
 template <bool kCluster = false>
 __device__ __forceinline__ bool wait1(unsigned long long& b, uint32_t parity,
