@@ -458,78 +458,76 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
     } else if (warp == 1) {
       // ------------------------------------------------------- QK (CTA 0)
-      const uint32_t id2 = idesc_bf16(128, 128, false), id1 = idesc_bf16(128, 64, false);
-      const uint64_t ring_d = sdesc_sw128(smem_u32(sl.ring[0]), 0, 1024);
-      const uint64_t rope_d = sdesc_sw128(smem_u32(sl.q_rope), 0, 1024);
-      int ent = 0, tc = 0, pieces = 0;
-      // debug: ml_free completes only after an output is written, so this
-      // bounded wait runs out and both CTAs leave through their give-up paths
-      if (ok && (debug_bits(err) & kDbgStallMla)) ok = wait32(ctl.ml_free, 0, abort_flag, err);
-      while (ok && walk.next(A, p, x)) {
-        for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
-          const int sb = tc & 1;
-          if (tc >= 2 && !(ok = wait32(ctl.s_empty[sb], ((tc >> 1) + 1) & 1, abort_flag, err)))
-            break;
-          tc_fence_after();
-          const uint32_t d = tmem + 128 * sb;
-          const uint32_t id = tile_units(x, t) > 1 ? id2 : id1;
-          const bool first = t == p.t0;
-          // an entry's barrier is asked for before the MMAs of the one before
-          // it are issued, so that a satisfied wait costs nothing after them
-          bool there = !first && mbar_try_wait(smem_u32(&ctl.k_full[ent & (kRing - 1)]),
-                                               (ent / kRing) & 1);
-#pragma unroll 1
-          for (int j = 0; j < kQPairs; ++j, ++ent) {
-            if (first) {                                // Q has left its place in the ring
-              if (!(ok = wait32(ctl.q_ready[j], pieces & 1, abort_flag, err))) break;
-              if (lane == 0) mbar_arrive(smem_u32(&ctl.k_empty[ent & (kRing - 1)]));
-              ++ent;
-              tc_fence_after();
-            }
-            const int st = ent & (kRing - 1);
-            if (!__all_sync(0xffffffffu, there) &&
-                !(ok = wait32(ctl.k_full[st], (ent / kRing) & 1, abort_flag, err)))
+      // One thread. The barriers of the next entry and of the next tile's
+      // buffer are asked for before the MMAs ahead of them are issued, so that
+      // a satisfied wait costs nothing after them.
+      if (elect_one()) {
+        const uint32_t id2 = idesc_bf16(128, 128, false), id1 = idesc_bf16(128, 64, false);
+        const uint64_t ring_d = sdesc_sw128(smem_u32(sl.ring[0]), 0, 1024);
+        const uint64_t rope_d = sdesc_sw128(smem_u32(sl.q_rope), 0, 1024);
+        const uint32_t k_full = smem_u32(&ctl.k_full[0]), k_empty = smem_u32(&ctl.k_empty[0]);
+        int ent = 0, tc = 0, pieces = 0;
+        auto ask = [&](int e) {
+          return mbar_try_wait(k_full + 8 * (e & (kRing - 1)), (e / kRing) & 1);
+        };
+        auto full = [&](int e, bool there) {
+          return there || wait1(ctl.k_full[e & (kRing - 1)], (e / kRing) & 1, abort_flag, err);
+        };
+        // debug: ml_free completes only after an output is written, so this
+        // bounded wait runs out and both CTAs leave through their give-up paths
+        if (ok && (debug_bits(err) & kDbgStallMla)) ok = wait1(ctl.ml_free, 0, abort_flag, err);
+        bool room = true;                               // the tile's buffer of logits is free
+        while (ok && walk.next(A, p, x)) {
+          for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
+            const int sb = tc & 1;
+            const uint32_t d = tmem + 128 * sb;
+            const uint32_t id = tile_units(x, t) > 1 ? id2 : id1;
+            const bool first = t == p.t0;
+            bool there = !first && ask(ent);
+            if (!room && !(ok = wait1(ctl.s_empty[sb], ((tc >> 1) + 1) & 1, abort_flag, err)))
               break;
-            there = (!first || j + 1 == kQPairs) &&
-                    mbar_try_wait(smem_u32(&ctl.k_full[(ent + 1) & (kRing - 1)]),
-                                  ((ent + 1) / kRing) & 1);
-            const uint64_t kd = ring_d + st * (kEntry >> 4);
-            const uint32_t qc = tmem + kColQ + 64 * j;
-            if (elect_one()) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < kQPairs; ++j, ++ent) {
+              if (first) {                              // Q has left its place in the ring
+                if (!(ok = wait1(ctl.q_ready[j], pieces & 1, abort_flag, err))) break;
+                mbar_arrive(k_empty + 8 * (ent & (kRing - 1)));
+                ++ent;
+                tc_fence_after();
+              }
+              if (!(ok = full(ent, there))) break;
+              there = (!first || j + 1 == kQPairs) && ask(ent + 1);
+              const int st = ent & (kRing - 1);
+              const uint64_t kd = ring_d + st * (kEntry >> 4);
+              const uint32_t qc = tmem + kColQ + 64 * j;
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)            // 16 dims: 8 TMEM columns of Q
                 mma_bf16_ts(d, qc + 8 * kk, kd + (kk >> 2) * (kAtom >> 4) + 2 * (kk & 3), id,
                             (j > 0 || kk > 0) ? 1u : 0u);
-              mma_commit(smem_u32(&ctl.k_empty[st]));
+              mma_commit(k_empty + 8 * st);
             }
-            __syncwarp();
-          }
-          if (!ok) break;
-          if (first && !(ok = wait32(ctl.rope_full, pieces & 1, abort_flag, err))) break;
-          const int st = ent & (kRing - 1);
-          if (!__all_sync(0xffffffffu, there) &&
-              !(ok = wait32(ctl.k_full[st], (ent / kRing) & 1, abort_flag, err)))
-            break;
-          ++ent;
-          const uint64_t kd = ring_d + st * (kEntry >> 4);
-          if (elect_one()) {
+            if (!ok) break;
+            if (first && !(ok = wait1(ctl.rope_full, pieces & 1, abort_flag, err))) break;
+            if (!(ok = full(ent, there))) break;
+            room = tc == 0 || mbar_try_wait(smem_u32(&ctl.s_empty[sb ^ 1]),
+                                            (((tc + 1) >> 1) + 1) & 1);
+            const int st = ent & (kRing - 1);
+            const uint64_t kd = ring_d + st * (kEntry >> 4);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) mma_bf16(d, rope_d + 2 * kk, kd + 2 * kk, id, 1u);
-            mma_commit(smem_u32(&ctl.k_empty[st]));
+            mma_commit(k_empty + 8 * st);
             mma_commit(smem_u32(&ctl.s_full[sb]));
             if (t + 1 == p.t1) mma_commit(smem_u32(&ctl.q_free));
+            ++ent;
           }
-          __syncwarp();
+          ++pieces;
         }
-        ++pieces;
-      }
-      if (!ok) {             // MMAs in flight read shared memory: wait for them
-        if (elect_one()) {
+        if (!ok) {           // MMAs in flight read shared memory: wait for them
           mma_commit(smem_u32(&ctl.o_done));
           mbar_drain(smem_u32(&ctl.o_done), 0);
         }
-        __syncwarp();
       }
+      __syncwarp();
     } else if (warp == 3) {
       // ----------------------------------------------- P to CTA 1 (CTA 0)
       if (lane == 0) {
@@ -729,55 +727,49 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
     } else if (warp == 1) {
       // ------------------------------------------------------- PV (CTA 1)
-      const uint32_t id = idesc_bf16(128, 256, true);
-      const uint64_t p_d = sdesc_sw128(smem_u32(so.p[0]), 0, 1024);
-      const uint64_t v_d = sdesc_sw128(smem_u32(so.v[0]), kUnitAtom, 1024);
-      int vc = 0, tc = 0, ac = 0;
-      unsigned cleaned = 0;                             // parity of each unit's uses of `clean`
-      while (ok && walk.next(A, p, x)) {
-        for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
-          const int n = tile_units(x, t);
-          if (!(ok = wait32(ctl.o_ok[tc & 3], (tc >> 2) & 1, abort_flag, err))) break;
-          tc_fence_after();
-          for (int u = 0; ok && u < n; ++u, ++ac) {
-            const int slot = ac & 3;
-            if (!(ok = wait32<true>(ctl.p_full[slot], (ac >> 2) & 1, abort_flag, err))) break;
-            if (2 * t + u < x.nu && unit_hidden(A, x, 2 * t + u) != 0ull) {
-              if (!(ok = wait32(ctl.clean[u], (cleaned >> u) & 1, abort_flag, err))) break;
-              cleaned ^= 1u << u;
-            }
-            const uint64_t pd = p_d + slot * (kAtom >> 4);
+      // One thread.
+      if (elect_one()) {
+        const uint32_t id = idesc_bf16(128, 256, true);
+        const uint64_t p_d = sdesc_sw128(smem_u32(so.p[0]), 0, 1024);
+        const uint64_t v_d = sdesc_sw128(smem_u32(so.v[0]), kUnitAtom, 1024);
+        int vc = 0, tc = 0, ac = 0;
+        unsigned cleaned = 0;                           // parity of each unit's uses of `clean`
+        while (ok && walk.next(A, p, x)) {
+          for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
+            const int n = tile_units(x, t);
+            if (!(ok = wait1(ctl.o_ok[tc & 3], (tc >> 2) & 1, abort_flag, err))) break;
+            tc_fence_after();
+            for (int u = 0; ok && u < n; ++u, ++ac) {
+              const int slot = ac & 3;
+              if (!(ok = wait1<true>(ctl.p_full[slot], (ac >> 2) & 1, abort_flag, err))) break;
+              if (2 * t + u < x.nu && unit_hidden(A, x, 2 * t + u) != 0ull) {
+                if (!(ok = wait1(ctl.clean[u], (cleaned >> u) & 1, abort_flag, err))) break;
+                cleaned ^= 1u << u;
+              }
+              const uint64_t pd = p_d + slot * (kAtom >> 4);
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h, ++vc) {
-              const int st = vc & 3;
-              if (!(ok = wait32(ctl.v_full[st], (vc >> 2) & 1, abort_flag, err))) break;
-              const uint64_t vd = v_d + st * (kVChunk >> 4);
-              if (elect_one()) {
+              for (int h = 0; h < 2; ++h, ++vc) {
+                const int st = vc & 3;
+                if (!(ok = wait1(ctl.v_full[st], (vc >> 2) & 1, abort_flag, err))) break;
+                const uint64_t vd = v_d + st * (kVChunk >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)          // 16 keys: 32 B of P, 2 KB of V
                   mma_bf16(tmem + 256 * h, pd + 2 * kk, vd + (kk * 2048 >> 4), id,
                            (t > p.t0 || u > 0 || kk > 0) ? 1u : 0u);
                 mma_commit(smem_u32(&ctl.v_empty[st]));
-                if (h == 1) {
-                  mma_commit(smem_u32(&ctl.p_free[slot]));
-                  if (u + 1 == n) {
-                    mma_commit(smem_u32(&ctl.pv_done[tc & 3]));
-                    if (t + 1 == p.t1) mma_commit(smem_u32(&ctl.o_done));
-                  }
-                }
               }
-              __syncwarp();
+              mma_commit(smem_u32(&ctl.p_free[slot]));
             }
+            mma_commit(smem_u32(&ctl.pv_done[tc & 3]));
           }
+          mma_commit(smem_u32(&ctl.o_done));
         }
-      }
-      if (!ok) {
-        if (elect_one()) {
+        if (!ok) {
           mma_commit(smem_u32(&ctl.q_free));
           mbar_drain(smem_u32(&ctl.q_free), 0);
         }
-        __syncwarp();
       }
+      __syncwarp();
     } else if (warp == 2 || warp == 3) {
       // ---- word to CTA 0: an atom has landed (warp 2), its slot is free (warp 3)
       if (lane == 0) {
