@@ -55,6 +55,7 @@ constexpr int kVChunk = 4 * kUnitAtom;          // 64 keys x 256 dims
 constexpr int kRing = 4;
 constexpr int kQPairs = 4;                      // Q dims [0, 512) live in TMEM, 128 at a time
 constexpr uint32_t kColQ = 256;                 // after two buffers of 128 logits
+constexpr int kPieces = 8;                      // pieces written down at a time
 constexpr int kPSlots = 4;
 constexpr int kVRing = 4;
 constexpr int kAhead = 3;                       // tiles of L2 prefetch, ahead of CTA 1's V
@@ -80,36 +81,6 @@ struct OutputSmem {                             // CTA 1
 };
 constexpr size_t kBig = std::max(sizeof(LogitsSmem), sizeof(OutputSmem));
 static_assert(kBig % 1024 == 0, "the control block follows the larger role's memory");
-
-struct Ctl {
-  // CTA 0
-  unsigned long long q_free;                    // the piece's last QK is done
-  unsigned long long q_ready[kQPairs];          // 128 dims of Q are in TMEM
-  unsigned long long rope_full;
-  unsigned long long k_full[kRing], k_empty[kRing];
-  unsigned long long s_full[2], s_empty[2];     // by tile parity
-  unsigned long long mx_bar[4];                 // both groups' maxima of a lane quarter
-  // by tile parity and unit, so that whoever waits on one sees every phase
-  unsigned long long p_own[2][2];               // a staged atom is written
-  unsigned long long p_ack[2][2];               // CTA 1 holds the atom: its staging is free
-  unsigned long long p_room[kPSlots];           // CTA 1 has room for another atom
-  unsigned long long ml_free;                   // CTA 1 has read ml
-  // CTA 1
-  unsigned long long v_full[kVRing], v_empty[kVRing];
-  unsigned long long p_full[kPSlots], p_free[kPSlots];
-  unsigned long long al_full[4];                // a tile's rescale factors have landed
-  unsigned long long o_ok[4];                   // O is ready for a tile's PV
-  unsigned long long clean[2];                  // V of a tile's unit with hidden keys is ready
-  unsigned long long pv_done[4];
-  unsigned long long o_done;
-  unsigned long long ml_full;
-  Share share;                                  // of the row tiles' weights
-  int progress;                                 // CTA 1: tiles whose V loads have begun
-  uint32_t tmem_base;
-  int abort_flag;
-};
-constexpr size_t kSmemBytes = kBig + sizeof(Ctl) + 1024;
-static_assert(kSmemBytes <= 232448, "fits the 227 KB of shared memory a CTA may use");
 
 // The bits a .. b of 0 .. 63 (none if a > b).
 __device__ __forceinline__ unsigned long long range_bits(int a, int b) {
@@ -204,58 +175,89 @@ __device__ __forceinline__ int entry_row(const RangeArgs& A, int entry) {
 }
 
 // A cluster's share, one piece (tiles [t0, t1) of a row tile) after another.
-// Every warp walks it on its own; all see the same pieces.
 struct Piece {
-  int item, t0, t1;
-  bool first, last;                             // holds the row tile's first, last tile
+  Item x;
   long long start;                              // the row tile's place in the weight list
+  int item;                                     // -1: no more pieces
+  int t0, t1;
+  bool first, last;                             // holds the row tile's first, last tile
 };
+static_assert(sizeof(Piece) % 4 == 0 && sizeof(Piece) <= 128, "at most a word a lane");
+
 struct Walk {
   int item, off, left;
   long long start;
-  __device__ __forceinline__ Walk(const Share& s)
+  __device__ __forceinline__ explicit Walk(const Share& s)
       : item(s.item), off(s.off), left(s.left), start(s.start) {}
-  // Out of line: every role calls it, once a piece.
-  __device__ __noinline__ bool step(const RangeArgs& A, Piece& p, Item& x) {
+  __device__ __forceinline__ Piece next(const RangeArgs& A) {
+    Piece p;
+    p.item = -1;
     if (A.whole) {
       // later rows of a prefill see more keys: they go first
-      if (item >= A.items) return false;
-      p.item = A.items - 1 - item;
-      item += A.clusters;
-      x = item_geom(A, p.item);
-      p.t0 = 0;
-      p.t1 = x.tiles;
-      p.first = p.last = true;
-      return true;
+      if (item < A.items) {
+        p.item = A.items - 1 - item;
+        item += A.clusters;
+        p.x = item_geom(A, p.item);
+        p.t0 = 0;
+        p.t1 = p.x.tiles;
+        p.first = p.last = true;
+      }
+      return p;
     }
     while (left > 0 && item < A.items) {
-      x = item_geom(A, item);
-      const int weight = x.tiles + kItemCost;
+      p.x = item_geom(A, item);
+      const int weight = p.x.tiles + kItemCost;
       const int take = min(weight - off, left);
-      p.item = item;
       p.t0 = max(0, off - kItemCost);
       p.t1 = off + take - kItemCost;
       p.start = start;
       p.first = p.t0 == 0;
-      p.last = p.t1 == x.tiles;
+      p.last = p.t1 == p.x.tiles;
       left -= take;
       off = 0;
       start += weight;
       ++item;
-      if (p.t1 > p.t0) return true;
+      if (p.t1 > p.t0) {
+        p.item = item - 1;
+        break;
+      }
     }
-    return false;
-  }
-  // (through copies, so that the caller's stay in registers)
-  __device__ __forceinline__ bool next(const RangeArgs& A, Piece& p, Item& x) {
-    Piece p1;
-    Item x1;
-    const bool more = step(A, p1, x1);
-    p = p1;
-    x = x1;
-    return more;
+    return p;
   }
 };
+
+struct Ctl {
+  Piece piece[kPieces];                         // by piece number
+  // CTA 0
+  unsigned long long q_free;                    // the piece's last QK is done
+  unsigned long long q_ready[kQPairs];          // 128 dims of Q are in TMEM
+  unsigned long long rope_full;
+  unsigned long long k_full[kRing], k_empty[kRing];
+  unsigned long long s_full[2], s_empty[2];     // by tile parity
+  unsigned long long mx_bar[4];                 // both groups' maxima of a lane quarter
+  // by tile parity and unit, so that whoever waits on one sees every phase
+  unsigned long long p_own[2][2];               // a staged atom is written
+  unsigned long long p_ack[2][2];               // CTA 1 holds the atom: its staging is free
+  unsigned long long p_room[kPSlots];           // CTA 1 has room for another atom
+  unsigned long long ml_free;                   // CTA 1 has read ml
+  // CTA 1
+  unsigned long long v_full[kVRing], v_empty[kVRing];
+  unsigned long long p_full[kPSlots], p_free[kPSlots];
+  unsigned long long al_full[4];                // a tile's rescale factors have landed
+  unsigned long long o_ok[4];                   // O is ready for a tile's PV
+  unsigned long long clean[2];                  // V of a tile's unit with hidden keys is ready
+  unsigned long long pv_done[4];
+  unsigned long long o_done;
+  unsigned long long ml_full;
+  Share share;                                  // of the row tiles' weights
+  unsigned long long piece_full[kPieces];
+  unsigned long long piece_done[kPieces];       // CTA 1: the piece's output is on its way
+  int progress;                                 // CTA 1: tiles whose V loads have begun
+  uint32_t tmem_base;
+  int abort_flag;
+};
+constexpr size_t kSmemBytes = kBig + sizeof(Ctl) + 1024;
+static_assert(kSmemBytes <= 232448, "fits the 227 KB of shared memory a CTA may use");
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
@@ -328,6 +330,10 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       init(ctl.s_full[i], 1);
       init(ctl.s_empty[i], 8);
     }
+    for (int i = 0; i < kPieces; ++i) {
+      init(ctl.piece_full[i], 1);
+      init(ctl.piece_done[i], 1);
+    }
     init(ctl.ml_free, 8);
     init(ctl.o_done, 1);
     init(ctl.clean[0], 8);
@@ -354,10 +360,21 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
   volatile int* abort_flag = &ctl.abort_flag;
-  Walk walk(ctl.share);
-  Piece p;
-  Item x;
   bool ok = *abort_flag == 0;
+  // The pieces, written down by CTA 1's warp 13 for every role of both CTAs (the
+  // arithmetic is cold code that each role would wait for between two pieces).
+  Piece p;
+  Item& x = p.x;
+  int pieces = 0;                               // of this role so far
+  auto next_piece = [&](bool whole_warp) {
+    unsigned long long& full = ctl.piece_full[pieces & (kPieces - 1)];
+    const uint32_t parity = (pieces / kPieces) & 1;
+    ok = ok && (whole_warp ? wait32<true>(full, parity, abort_flag, err)
+                           : wait1<true>(full, parity, abort_flag, err));
+    if (!ok) return false;
+    p = ctl.piece[pieces & (kPieces - 1)];
+    return p.item >= 0;
+  };
 
   if (rank == 0) {
     if (warp == 0 || warp == 2) {
@@ -367,8 +384,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // piece's first tile each K entry follows the Q entry it meets.
       const int par = warp >> 1;
       if (lane == 0) {
-        int ent = 0, pieces = 0;
-        while (ok && walk.next(A, p, x)) {
+        int ent = 0;
+        for (; next_piece(false); ++pieces) {
           const int q_row = static_cast<int>(x.row0);
           int e0 = unit_entry(A, x, 2 * p.t0), e1 = unit_entry(A, x, 2 * p.t0 + 1);
           for (int t = p.t0; ok && t < p.t1; ++t) {
@@ -410,7 +427,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               }
             }
           }
-          ++pieces;
         }
         if (!ok) {           // let the loads in flight land before this CTA leaves
           for (int c = max(0, ent - kRing); c < ent; ++c)
@@ -426,8 +442,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // been consumed, so the barriers waited on below are in the phase before.)
       const int r = 32 * (warp & 3) + lane;
       const uint32_t q_cols = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kColQ;
-      int ent = 0, pieces = 0;
-      while (ok && walk.next(A, p, x)) {
+      int ent = 0;
+      for (; next_piece(true); ++pieces) {
         if (pieces > 0 && !(ok = wait32(ctl.q_free, (pieces - 1) & 1, abort_flag, err))) break;
         tc_fence_after();
 #pragma unroll 1
@@ -454,7 +470,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           if (lane == 0) mbar_arrive(smem_u32(&ctl.q_ready[j]));
         }
         ent += 5 * (p.t1 - p.t0) + kQPairs;
-        ++pieces;
       }
     } else if (warp == 1) {
       // ------------------------------------------------------- QK (CTA 0)
@@ -466,7 +481,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint64_t ring_d = sdesc_sw128(smem_u32(sl.ring[0]), 0, 1024);
         const uint64_t rope_d = sdesc_sw128(smem_u32(sl.q_rope), 0, 1024);
         const uint32_t k_full = smem_u32(&ctl.k_full[0]), k_empty = smem_u32(&ctl.k_empty[0]);
-        int ent = 0, tc = 0, pieces = 0;
+        int ent = 0, tc = 0;
         auto ask = [&](int e) {
           return mbar_try_wait(k_full + 8 * (e & (kRing - 1)), (e / kRing) & 1);
         };
@@ -477,7 +492,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // bounded wait runs out and both CTAs leave through their give-up paths
         if (ok && (debug_bits(err) & kDbgStallMla)) ok = wait1(ctl.ml_free, 0, abort_flag, err);
         bool room = true;                               // the tile's buffer of logits is free
-        while (ok && walk.next(A, p, x)) {
+        for (; next_piece(false); ++pieces) {
           for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
             const int sb = tc & 1;
             const uint32_t d = tmem + 128 * sb;
@@ -520,7 +535,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (t + 1 == p.t1) mma_commit(smem_u32(&ctl.q_free));
             ++ent;
           }
-          ++pieces;
         }
         if (!ok) {           // MMAs in flight read shared memory: wait for them
           mma_commit(smem_u32(&ctl.o_done));
@@ -533,7 +547,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (lane == 0) {
         int a = 0, tc = 0;
         unsigned sent = 0;                              // parity of each staging's count
-        while (ok && walk.next(A, p, x)) {
+        for (; next_piece(false); ++pieces) {
           for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
             const int g = tc & 1, n = tile_units(x, t);
 #pragma unroll 1
@@ -574,9 +588,9 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const int r = 32 * wq + lane;                     // row = TMEM lane
       const uint32_t lanes = static_cast<uint32_t>(32 * wq) << 16;
       const float2 scale2 = make_float2(A.sm_scale_log2, A.sm_scale_log2);
-      int tc = 0, pieces = 0;
+      int tc = 0;
       unsigned acked = 3u;                              // parity of each staging's uses, before the first
-      while (ok && walk.next(A, p, x)) {
+      for (; next_piece(true); ++pieces) {
         const int pos = x.pos0 + r / A.H;
         const int hi = r < x.nrows ? min(pos, x.last) : -1;
         const int lo = A.window ? pos - A.window + 1 : 0;
@@ -598,16 +612,27 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
           const uint32_t s_cols = tmem + lanes + 128 * b + 64 * g;
           const bool first = t == p.t0;
+          // the staging is free once CTA 1 holds what it held (a barrier not
+          // yet used passes for the phase before its first)
+          if (g < n) {
+            if (!(ok = wait32<true>(ctl.p_ack[b][g], (acked >> b) & 1, abort_flag, err))) break;
+            acked ^= 1u << b;
+          }
+          if (!(ok = wait32(ctl.s_full[b], (tc >> 1) & 1, abort_flag, err))) break;
+          tc_fence_after();
           uint8_t* row = sl.p[b][g] + r * 128;
-          float mx = -INFINITY;
-          float2 sum2;
-          // P = exp2(z - base) of the unit into the staging, its sum, and the
-          // unit's maximum of the raw logits
-          auto form = [&](float base) {
+          float mx = -INFINITY, alpha = 1.f;
+          float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+          for (int round = 0; round < 2; ++round) {
+            // P = exp2(z - m) of the unit into the staging (not in the first
+            // tile's first round), its sum, and the unit's maximum
+            const bool form = !first || round == 1;
+            const float base = m == -INFINITY ? 0.f : m;
             const float2 base2 = make_float2(-base, -base);
             sum2 = make_float2(0.f, 0.f);
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < 2 && g < n; ++h) {
               float s[32];
               tmem_ld32(s_cols + 32 * h, s);
               const unsigned bits = static_cast<unsigned>(see >> (32 * h));
@@ -620,6 +645,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
               for (int e = 0; e < 32; ++e) pm[e & 3] = fmaxf(pm[e & 3], s[e]);
               mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+              if (!form) continue;
               // row r of the atom: 128 B, 16-B chunk c at chunk c ^ (r % 8)
 #pragma unroll
               for (int c = 0; c < 4; ++c) {
@@ -638,43 +664,22 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     make_uint4(pk[0], pk[1], pk[2], pk[3]);
               }
             }
-          };
-          // the staging is free once CTA 1 holds what it held (a barrier not
-          // yet used passes for the phase before its first)
-          if (g < n) {
-            if (!(ok = wait32<true>(ctl.p_ack[b][g], (acked >> b) & 1, abort_flag, err))) break;
-            acked ^= 1u << b;
+            if (round == 1) break;
+            // the row's maximum over both units
+            sl.mx[b][g][r] = mx;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctl.mx_bar[wq]));
+            if (!(ok = wait32(ctl.mx_bar[wq], tc & 1, abort_flag, err))) break;
+            const float top = fmaxf(mx, sl.mx[b][g ^ 1][r]) * A.sm_scale_log2;
+            const float m_new = top > m + kRebase ? top : m;
+            const bool moved = m_new != m;
+            if (moved && m > -INFINITY) alpha = fast_exp2(m - m_new);
+            m = m_new;
+            if (!first && !__any_sync(0xffffffffu, moved)) break;
           }
-          if (!(ok = wait32(ctl.s_full[b], (tc >> 1) & 1, abort_flag, err))) break;
-          tc_fence_after();
-          if (g < n) {
-            if (first) {
-#pragma unroll 1
-              for (int h = 0; h < 2; ++h) {
-                float s[32];
-                tmem_ld32(s_cols + 32 * h, s);
-                const unsigned bits = static_cast<unsigned>(see >> (32 * h));
-#pragma unroll
-                for (int e = 0; e < 32; ++e) mx = fmaxf(mx, (bits >> e) & 1u ? s[e] : -INFINITY);
-              }
-            } else {
-              form(m == -INFINITY ? 0.f : m);
-            }
-          }
-          // the row's maximum over both units
-          sl.mx[b][g][r] = mx;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl.mx_bar[wq]));
-          if (!(ok = wait32(ctl.mx_bar[wq], tc & 1, abort_flag, err))) break;
-          const float top = fmaxf(mx, sl.mx[b][g ^ 1][r]) * A.sm_scale_log2;
-          const float m_new = top > m + kRebase ? top : m;
-          const bool moved = m_new != m;
-          const float alpha = moved && m > -INFINITY ? fast_exp2(m - m_new) : 1.f;
-          m = m_new;
-          if (g < n && (first || __any_sync(0xffffffffu, moved)))
-            form(m == -INFINITY ? 0.f : m);
+          if (!ok) break;
           if (g == 0) sl.alpha[b][r] = alpha;
-          l = g < n ? l * alpha + (sum2.x + sum2.y) : l * alpha;
+          l = l * alpha + (sum2.x + sum2.y);
           fence_proxy_async_smem();                     // generic writes -> bulk-copy reads
           tc_fence_before();
           __syncwarp();
@@ -692,7 +697,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         st_cluster_f32(ml + 4, l);
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctl.ml_full), peer));
-        ++pieces;
       }
     }
   } else {
@@ -702,7 +706,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         int vc = 0;
         volatile int* progress = &ctl.progress;
         int tc = 0;
-        while (ok && walk.next(A, p, x)) {
+        for (; next_piece(false); ++pieces) {
+          // table entries are loaded a tile before they are used
           int e0 = unit_entry(A, x, 2 * p.t0), e1 = unit_entry(A, x, 2 * p.t0 + 1);
           for (int t = p.t0; ok && t < p.t1; ++t) {
             const int n = tile_units(x, t);
@@ -734,7 +739,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint64_t v_d = sdesc_sw128(smem_u32(so.v[0]), kUnitAtom, 1024);
         int vc = 0, tc = 0, ac = 0;
         unsigned cleaned = 0;                           // parity of each unit's uses of `clean`
-        while (ok && walk.next(A, p, x)) {
+        for (; next_piece(false); ++pieces) {
           for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
             const int n = tile_units(x, t);
             if (!(ok = wait1(ctl.o_ok[tc & 3], (tc >> 2) & 1, abort_flag, err))) break;
@@ -774,7 +779,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // ---- word to CTA 0: an atom has landed (warp 2), its slot is free (warp 3)
       if (lane == 0) {
         int a = 0, tc = 0;
-        while (ok && walk.next(A, p, x)) {
+        for (; next_piece(false); ++pieces) {
           for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
             const int n = tile_units(x, t);
 #pragma unroll 1
@@ -801,9 +806,11 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // V (CTA 0 is about two tiles ahead of that). One warp's plain prefetches:
       // bulk ones go through the TMA engine, whose time CTA 1 needs for V
       // (64 x 32768: 731 us with them, 635 us with none).
+      // (It may fall behind, so it works out the pieces by itself.)
       volatile int* progress = &ctl.progress;
+      Walk walk(ctl.share);
       int tc = 0;
-      while (ok && walk.next(A, p, x)) {
+      while (ok && (p = walk.next(A)).item >= 0) {
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
           const unsigned long long t0 = globaltimer();
           while (*progress + kAhead < tc && ok) {
@@ -820,16 +827,42 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
       }
+    } else if (warp == 13) {
+      // -------------------------------------------- the pieces (CTA 1)
+      // Piece k is written once the output of piece k - 4 is on its way. The
+      // place it takes was piece k - 8's, which every role has copied by then:
+      // no role is more than four atoms of P behind the output, and a piece
+      // has at least one.
+      Walk walk(ctl.share);
+      for (;; ++pieces) {
+        const int done = pieces - kPieces / 2;
+        if (!(ok = ok && (done < 0 || wait32(ctl.piece_done[done & (kPieces - 1)],
+                                             (done / kPieces) & 1, abort_flag, err))))
+          break;
+        p = walk.next(A);
+        const int slot = pieces & (kPieces - 1);
+        if (lane == 0) ctl.piece[slot] = p;
+        __syncwarp();
+        if (lane < static_cast<int>(sizeof(Piece) / 4)) {
+          const float* w = reinterpret_cast<const float*>(&ctl.piece[slot]) + lane;
+          st_cluster_f32(mapa(smem_u32(w), peer), *w);
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ctl.piece_full[slot]));
+          mbar_arrive_remote(mapa(smem_u32(&ctl.piece_full[slot]), peer));
+        }
+        if (p.item < 0) break;
+      }
     } else if (warp < 12) {
       // ------------------------------------- rescale and output (CTA 1)
       const int g = (warp - 4) >> 2;                    // half of the 512 value dims
       const int wq = warp & 3;
       const int r = 32 * wq + lane;
       const uint32_t o_cols = tmem + (static_cast<uint32_t>(32 * wq) << 16) + 256 * g;
-      int tc = 0, vc = 0, pieces = 0;
+      int tc = 0, vc = 0;
       bool recorded = false;
-      bool more = ok && walk.next(A, p, x);
-      while (ok && more) {
+      for (; next_piece(true); ++pieces) {
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
           const int n = tile_units(x, t);
           const int sl4 = tc & 3;
@@ -905,10 +938,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         (a1.x > -INFINITY ? a1.y * fast_exp2(a1.x - m) : a1.y);
         if (!(ok = wait32(ctl.o_done, pieces & 1, abort_flag, err))) break;
         tc_fence_after();
-        // the next piece is worked out before this one's stores fill the queues
-        Piece p_next;
-        Item x_next;
-        more = walk.next(A, p_next, x_next);
         const bool valid = r < x.nrows;
         if (p.first && p.last) {
           const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -973,9 +1002,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             recorded = true;
           }
         }
-        ++pieces;
-        p = p_next;
-        x = x_next;
+        if (threadIdx.x == 128)
+          mbar_arrive(smem_u32(&ctl.piece_done[pieces & (kPieces - 1)]));
       }
       if (threadIdx.x == 128 && !recorded && A.rec) A.rec[cluster] = make_int2(-1, 0);
     }
