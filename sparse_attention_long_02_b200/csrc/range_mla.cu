@@ -1018,35 +1018,62 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 // Joins the parts of a cut row tile. CTA (c, y, z): the row tile whose first
-// tile closes cluster c's share, rows 8 y .. 8 y + 7, value dims 128 z on.
+// tile closes cluster c's share, rows 32 y on, value dims 32 z on. The parts'
+// weights are worked out once a row; then each warp adds up four dims of 32
+// rows (512 consecutive bytes of a part), eight parts in flight.
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads) range_join_kernel(const RangeArgs A) {
+  __shared__ float weight[kMaxClusters][32], top[8][32], sum[8][32];
   const int c = static_cast<int>(blockIdx.x);
   const int2 rec = A.rec[c];
-  if (rec.x < 0 || launch_aborted(A.err)) return;
+  if (__syncthreads_or(rec.x < 0 || launch_aborted(A.err))) return;
   const Item x = item_geom(A, rec.x);
-  const int r = 8 * static_cast<int>(blockIdx.y) + static_cast<int>(threadIdx.x & 7);
-  if (r >= x.nrows) return;
-  const int c4 = 32 * static_cast<int>(blockIdx.z) + static_cast<int>(threadIdx.x >> 3);
+  const int warp = warp_id(), lane = lane_id();
+  const int r0 = 32 * static_cast<int>(blockIdx.y), r = r0 + lane;
+  if (r0 >= x.nrows) return;
   const int n = rec.y - c + 1;                  // parts: slot 1 of c, slot 0 of c+1 .. rec.y
   auto slot = [&](int i) { return static_cast<long long>(2 * (c + i) + (i == 0 ? 1 : 0)); };
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) m = fmaxf(m, A.part_ml[slot(i) * A.rows_pad + r].x);
+  const bool valid = r < x.nrows;
+  float m = -INFINITY, l = 0.f;
+  for (int i = warp; i < n; i += 8)
+    if (valid) m = fmaxf(m, A.part_ml[slot(i) * A.rows_pad + r].x);
+  top[warp][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, top[w][lane]);
   const float base = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = 0; i < n; ++i) {
-    const float2 ml = A.part_ml[slot(i) * A.rows_pad + r];
-    const float4 v = A.part_o[(slot(i) * 128 + c4) * A.rows_pad + r];
+  for (int i = warp; i < n; i += 8) {
+    const float2 ml = valid ? A.part_ml[slot(i) * A.rows_pad + r] : make_float2(-INFINITY, 0.f);
     const float w = fast_exp2(ml.x - base);
-    l += ml.x == -INFINITY ? ml.y : w * ml.y;
+    weight[i][lane] = w;
+    l += ml.x == -INFINITY ? ml.y : w * ml.y;   // (a NaN sum of a part stays one)
+  }
+  sum[warp][lane] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) l += sum[w][lane];
+  if (!valid) return;
+  const int c4 = 8 * static_cast<int>(blockIdx.z) + warp;
+  const float4* part = A.part_o + static_cast<long long>(c4) * A.rows_pad + r;
+  const long long pitch = 128ll * A.rows_pad;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](const float4& v, float w) {
     o.x += w * v.x;
     o.y += w * v.y;
     o.z += w * v.z;
     o.w += w * v.w;
+  };
+  add(part[slot(0) * pitch], weight[0][lane]);
+  int i = 1;
+  for (; i + 8 <= n; i += 8) {
+    float4 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = part[slot(i + k) * pitch];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) add(v[k], weight[i + k][lane]);
   }
+  for (; i < n; ++i) add(part[slot(i) * pitch], weight[i][lane]);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv);
   const __nv_bfloat162 b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
@@ -1107,7 +1134,7 @@ cudaError_t launch_range_mla(const RangeArgs& a_in, cudaStream_t st) {
   range_mla_kernel<<<2 * a.clusters, kThreads, kSmemBytes, st>>>(tq, tk, tv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.rec) return e;
-  range_join_kernel<<<dim3(a.clusters, a.rows_pad / 8, 4), kJoinThreads, 0, st>>>(a);
+  range_join_kernel<<<dim3(a.clusters, (a.rows_pad + 31) / 32, 16), kJoinThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
