@@ -43,7 +43,7 @@ struct MassSmem {
   float lse2[8][128];                           // the rows' normalisers in log2 units
   int pos[8][128];                              // the rows' positions, -1: gives nothing
   Share share;
-  long long sums[kThreads / 32];
+  long long sums[2 * (kThreads / 32)];
   unsigned long long q_full, q_free;
   unsigned long long k_full[kRing], k_empty[kRing];
   unsigned long long s_full[2], s_empty[2];
@@ -88,7 +88,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   unsigned* err = A.err;
   const int warp = warp_id(), lane = lane_id();
   find_share<kThreads>(sm.share, sm.sums, A.B, static_cast<int>(blockIdx.x),
-                       static_cast<int>(gridDim.x), kMinShare, [&](int b) {
+                       static_cast<int>(gridDim.x), kMinShare, 0, [&](int b) {
                          const int len = A.seq_len[b];
                          if (blockIdx.x == 0 && (len < 0 || len > A.max_blocks * 64))
                            raise_error(err, kErrBounds);

@@ -31,7 +31,8 @@
 // so neither role waits for the other's loads.
 //
 // Work split. The tiles of all row tiles form one list; each cluster takes an
-// equal share of it, wherever it begins and ends. A row tile inside one share
+// equal share of it, wherever it begins and ends (or whole row tiles in turn,
+// where that is as fast as equal shares and the join they need). A row tile inside one share
 // is written directly; one cut over several clusters leaves its parts (fp32
 // sums of p v with the row's maximum and sum) in the workspace, which
 // range_join_kernel combines: with m = max m_i, l = sum l_i 2^(m_i - m),
@@ -58,12 +59,15 @@ constexpr uint32_t kColQ = 256;                 // after two buffers of 128 logi
 constexpr int kPieces = 8;                      // pieces written down at a time
 constexpr int kPSlots = 4;
 constexpr int kVRing = 4;
-constexpr int kAhead = 3;                       // tiles of L2 prefetch, ahead of CTA 1's V
+constexpr int kAhead = 2;                       // tiles of L2 prefetch, ahead of CTA 1's V
 constexpr float kRebase = 8.0f;                 // lazy rescale threshold (log2 units)
 constexpr int kMaxClusters = 74;                // two CTAs on each of 148 SMs
 constexpr int kScanItems = 16384;               // row tiles a cluster scans for its share
-constexpr int kItemCost = 1;                    // a row tile's fixed cost, in tiles
+constexpr int kItemCost = 3;                    // a row tile's fixed cost, in tiles
 constexpr int kMinShare = 2;                    // tiles (and fixed costs) a cluster takes at least
+// What cutting row tiles costs, in tiles: where there are fewer of them than
+// clusters a cluster writes one part, else two.
+constexpr int kCutCostFew = 3, kCutCostMany = 7;
 
 struct LogitsSmem {                             // CTA 0
   uint8_t ring[kRing][kEntry];                  // K, and Q on its way to TMEM
@@ -101,7 +105,9 @@ struct Item {
   const int* table;                             // the sequence's block table (paged)
 };
 
-__device__ __forceinline__ Item item_geom(const RangeArgs& A, int i) {
+// (Out of line: the search for the share, which calls it first, has then
+// fetched its code for the warp that walks the pieces.)
+__device__ __noinline__ Item item_geom(const RangeArgs& A, int i) {
   Item x;
   int nq;
   if (A.block_table) {
@@ -185,14 +191,14 @@ struct Piece {
 static_assert(sizeof(Piece) % 4 == 0 && sizeof(Piece) <= 128, "at most a word a lane");
 
 struct Walk {
-  int item, off, left;
+  int item, off, left, whole;
   long long start;
   __device__ __forceinline__ explicit Walk(const Share& s)
-      : item(s.item), off(s.off), left(s.left), start(s.start) {}
+      : item(s.item), off(s.off), left(s.left), whole(s.whole), start(s.start) {}
   __device__ __forceinline__ Piece next(const RangeArgs& A) {
     Piece p;
     p.item = -1;
-    if (A.whole) {
+    if (whole) {
       // later rows of a prefill see more keys: they go first
       if (item < A.items) {
         p.item = A.items - 1 - item;
@@ -295,10 +301,12 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (threadIdx.x == 0) {
       ctl.share = Share{};
       ctl.share.item = cluster;
+      ctl.share.whole = 1;
     }
   } else {
     find_share<kThreads>(ctl.share, reinterpret_cast<long long*>(big), A.items, cluster,
-                         A.clusters, kMinShare, [&](int i) {
+                         A.clusters, kMinShare,
+                         A.items < A.clusters ? kCutCostFew : kCutCostMany, [&](int i) {
                            if (A.block_table && blockIdx.x == 0) {
                              const int len = A.seq_len[i / A.per_seq];
                              if (len < 0 || len > A.max_blocks * 64) raise_error(err, kErrBounds);
@@ -356,6 +364,10 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   fence_proxy_async_smem();               // find_share's scratch, before loads land there
   tc_fence_before();
   __syncthreads();
+  Walk walk(ctl.share);
+  Piece p;
+  if (rank == 1 && warp == 13) p = walk.next(A);
+  __syncwarp();
   cluster_sync();          // barriers of both CTAs initialised before any remote arrive
   tc_fence_after();
   const uint32_t tmem = ctl.tmem_base;
@@ -363,7 +375,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   bool ok = *abort_flag == 0;
   // The pieces, written down by CTA 1's warp 13 for every role of both CTAs (the
   // arithmetic is cold code that each role would wait for between two pieces).
-  Piece p;
   Item& x = p.x;
   int pieces = 0;                               // of this role so far
   auto next_piece = [&](bool whole_warp) {
@@ -808,9 +819,13 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // (64 x 32768: 731 us with them, 635 us with none).
       // (It may fall behind, so it works out the pieces by itself.)
       volatile int* progress = &ctl.progress;
-      Walk walk(ctl.share);
       int tc = 0;
       while (ok && (p = walk.next(A)).item >= 0) {
+        {
+          const char* at = reinterpret_cast<const char*>(A.q + x.row0 * 576);
+          for (int i = lane; i < 9 * x.nrows; i += 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * i));
+        }
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
           const unsigned long long t0 = globaltimer();
           while (*progress + kAhead < tc && ok) {
@@ -833,13 +848,12 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // place it takes was piece k - 8's, which every role has copied by then:
       // no role is more than four atoms of P behind the output, and a piece
       // has at least one.
-      Walk walk(ctl.share);
       for (;; ++pieces) {
         const int done = pieces - kPieces / 2;
         if (!(ok = ok && (done < 0 || wait32(ctl.piece_done[done & (kPieces - 1)],
                                              (done / kPieces) & 1, abort_flag, err))))
           break;
-        p = walk.next(A);
+        if (pieces > 0) p = walk.next(A);
         const int slot = pieces & (kPieces - 1);
         if (lane == 0) ctl.piece[slot] = p;
         __syncwarp();
@@ -1017,70 +1031,105 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   }
 }
 
-// Joins the parts of a cut row tile. CTA (c, y, z): the row tile whose first
-// tile closes cluster c's share, rows 32 y on, value dims 32 z on. The parts'
-// weights are worked out once a row; then each warp adds up four dims of 32
-// rows (512 consecutive bytes of a part), eight parts in flight.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) range_join_kernel(const RangeArgs A) {
+// Joins the parts of the cut row tiles. A task is 32 rows and 32 value dims of
+// a row tile (8 where it has many parts, which four warps then share); record c
+// names the row tile whose first tile closes cluster c's share. The parts'
+// weights are worked out once a row; then each warp adds up four dims of 32 rows
+// (512 consecutive bytes of a part), eight parts in flight.
+constexpr int kJoinThreads = 256, kJoinCtas = 5 * 148;
+constexpr int kJoinBatch = (kMaxClusters + 7) / 8;              // parts a warp weighs
+__global__ void __launch_bounds__(kJoinThreads, 5)
+range_join_kernel(const __grid_constant__ RangeArgs A) {
   __shared__ float weight[kMaxClusters][32], top[8][32], sum[8][32];
-  const int c = static_cast<int>(blockIdx.x);
-  const int2 rec = A.rec[c];
-  if (__syncthreads_or(rec.x < 0 || launch_aborted(A.err))) return;
-  const Item x = item_geom(A, rec.x);
+  __shared__ float4 partial[8][32];
+  __shared__ int2 recs[kMaxClusters];
   const int warp = warp_id(), lane = lane_id();
-  const int r0 = 32 * static_cast<int>(blockIdx.y), r = r0 + lane;
-  if (r0 >= x.nrows) return;
-  const int n = rec.y - c + 1;                  // parts: slot 1 of c, slot 0 of c+1 .. rec.y
-  auto slot = [&](int i) { return static_cast<long long>(2 * (c + i) + (i == 0 ? 1 : 0)); };
-  const bool valid = r < x.nrows;
-  float m = -INFINITY, l = 0.f;
-  for (int i = warp; i < n; i += 8)
-    if (valid) m = fmaxf(m, A.part_ml[slot(i) * A.rows_pad + r].x);
-  top[warp][lane] = m;
-  __syncthreads();
+  const bool skip = launch_aborted(A.err);
+  if (static_cast<int>(threadIdx.x) < A.clusters) recs[threadIdx.x] = A.rec[threadIdx.x];
+  if (__syncthreads_or(skip)) return;
+  const int row_blocks = (A.rows_pad + 31) >> 5;
+  int task = static_cast<int>(blockIdx.x);      // within the records from c on
+  for (int c = 0; c < A.clusters; ++c) {
+    const int2 rec = recs[c];
+    if (rec.x < 0) continue;
+    const int n = rec.y - c + 1;                // parts: slot 1 of c, slot 0 of c+1 .. rec.y
+    const int ways = n > 16 ? 4 : 1, across = 8 / ways;         // warps on one group of dims, groups
+    const int per_row = 128 / across, per_rec = per_row * row_blocks;
+    if (task >= per_rec) {
+      task -= per_rec;
+      continue;
+    }
+    const Item x = item_geom(A, rec.x);
+    auto slot = [&](int i) { return static_cast<long long>(2 * (c + i) + (i == 0 ? 1 : 0)); };
+    for (; task < per_rec; task += kJoinCtas) {
+      const int block = task / per_row, r = 32 * block + lane;
+      const bool valid = r < x.nrows;
+      float2 ml[kJoinBatch];
 #pragma unroll
-  for (int w = 0; w < 8; ++w) m = fmaxf(m, top[w][lane]);
-  const float base = m == -INFINITY ? 0.f : m;
-  for (int i = warp; i < n; i += 8) {
-    const float2 ml = valid ? A.part_ml[slot(i) * A.rows_pad + r] : make_float2(-INFINITY, 0.f);
-    const float w = fast_exp2(ml.x - base);
-    weight[i][lane] = w;
-    l += ml.x == -INFINITY ? ml.y : w * ml.y;   // (a NaN sum of a part stays one)
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const int i = warp + 8 * k;
+        ml[k] = valid && i < n ? A.part_ml[slot(i) * A.rows_pad + r] : make_float2(-INFINITY, 0.f);
+      }
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) m = fmaxf(m, ml[k].x);
+      __syncthreads();                          // the task before is done with the tables
+      top[warp][lane] = m;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < 8; ++w) m = fmaxf(m, top[w][lane]);
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int k = 0; k < kJoinBatch; ++k) {
+        const int i = warp + 8 * k;
+        if (i >= n) continue;
+        const float w = fast_exp2(ml[k].x - base);
+        weight[i][lane] = w;
+        l += ml[k].x == -INFINITY ? ml[k].y : w * ml[k].y;      // (a NaN sum of a part stays one)
+      }
+      sum[warp][lane] = l;
+      __syncthreads();
+      const int c4 = across * (task - block * per_row) + warp % across, way = warp / across;
+      const long long pitch = 128ll * A.rows_pad;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](const float4& v, float w) {
+        o.x += w * v.x;
+        o.y += w * v.y;
+        o.z += w * v.z;
+        o.w += w * v.w;
+      };
+      if (valid) {
+        const float4* part = A.part_o + static_cast<long long>(c4) * A.rows_pad + r;
+        int i = n * way / ways;
+        const int end = n * (way + 1) / ways;
+        for (; i + 8 <= end; i += 8) {
+          float4 v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) v[k] = part[slot(i + k) * pitch];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) add(v[k], weight[i + k][lane]);
+        }
+        for (; i < end; ++i) add(part[slot(i) * pitch], weight[i][lane]);
+      }
+      if (ways > 1) {
+        partial[warp][lane] = o;
+        __syncthreads();
+        for (int w = 1; w < ways && way == 0; ++w) add(partial[warp + w * across][lane], 1.f);
+      }
+      if (!valid || way != 0) continue;
+      l = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) l += sum[w][lane];
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+      *reinterpret_cast<uint2*>(A.out + (x.row0 + r) * 512 + 4 * c4) = make_uint2(
+          *reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      if (c4 == 0 && A.lse)
+        A.lse[x.row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    }
+    task -= per_rec;
   }
-  sum[warp][lane] = l;
-  __syncthreads();
-  l = 0.f;
-#pragma unroll
-  for (int w = 0; w < 8; ++w) l += sum[w][lane];
-  if (!valid) return;
-  const int c4 = 8 * static_cast<int>(blockIdx.z) + warp;
-  const float4* part = A.part_o + static_cast<long long>(c4) * A.rows_pad + r;
-  const long long pitch = 128ll * A.rows_pad;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](const float4& v, float w) {
-    o.x += w * v.x;
-    o.y += w * v.y;
-    o.z += w * v.z;
-    o.w += w * v.w;
-  };
-  add(part[slot(0) * pitch], weight[0][lane]);
-  int i = 1;
-  for (; i + 8 <= n; i += 8) {
-    float4 v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = part[slot(i + k) * pitch];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) add(v[k], weight[i + k][lane]);
-  }
-  for (; i < n; ++i) add(part[slot(i) * pitch], weight[i][lane]);
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-  const __nv_bfloat162 b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  *reinterpret_cast<uint2*>(A.out + (x.row0 + r) * 512 + 4 * c4) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  if (c4 == 0 && A.lse)
-    A.lse[x.row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 }  // namespace
@@ -1134,7 +1183,7 @@ cudaError_t launch_range_mla(const RangeArgs& a_in, cudaStream_t st) {
   range_mla_kernel<<<2 * a.clusters, kThreads, kSmemBytes, st>>>(tq, tk, tv, a);
   e = cudaGetLastError();
   if (e != cudaSuccess || !a.rec) return e;
-  range_join_kernel<<<dim3(a.clusters, (a.rows_pad + 31) / 32, 16), kJoinThreads, 0, st>>>(a);
+  range_join_kernel<<<kJoinCtas, kJoinThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 

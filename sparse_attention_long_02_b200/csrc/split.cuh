@@ -52,6 +52,7 @@ __device__ __forceinline__ bool wait32(unsigned long long& b, uint32_t parity,
 struct Share {
   long long total, start;                       // all weight; the weight before the first item
   int item, off, left, parts;                   // first item, offset into it, weight of the share
+  int whole;                                    // items c, c + parts_max, ... whole instead
 };
 
 // Where part c of `parts` begins. Totals that fit 32 bits, the usual ones, spare
@@ -64,20 +65,24 @@ __device__ __forceinline__ long long share_begin(long long total, int parts, int
 }
 
 // Finds share `c` of at most `parts_max`, each of `min_share` weight at least.
-// Called by all kThreads threads; `sums` is scratch for one number each; weight(i) is item
-// i's, at least 1 for some item. Ends with sh written by one thread: the caller
-// synchronises. Shares past the last part get item = items.
+// Where items taken whole, in turn, are as fast as equal shares and `cut_cost`
+// (weight that a cut costs; 0: always cut), the share says so instead. Called
+// by all kThreads threads; `sums` is scratch for two numbers a warp; weight(i)
+// is item i's. Ends with sh written by one thread: the caller synchronises.
+// Shares past the last part get item = items.
 template <int kThreads, typename Weight>
 __device__ __forceinline__ void find_share(Share& sh, long long* sums, int items, int c,
-                                           int parts_max, int min_share, Weight weight) {
+                                           int parts_max, int min_share, int cut_cost,
+                                           Weight weight) {
   const int tid = static_cast<int>(threadIdx.x);
   const int per = (items + kThreads - 1) / kThreads;
   const int i0 = min(items, tid * per), i1 = min(items, i0 + per);
   long long sum = 0;
-  int w_first = 0;
+  int w_first = 0, w_max = 0;
   for (int i = i0; i < i1; ++i) {
     const int w = weight(i);
     if (i == i0) w_first = w;
+    w_max = max(w_max, w);
     sum += w;
   }
   // exclusive prefix over the block: within warps, then over the warps' sums
@@ -87,11 +92,15 @@ __device__ __forceinline__ void find_share(Share& sh, long long* sums, int items
     const long long y = __shfl_up_sync(0xffffffffu, before, o);
     if (lane_id() >= o) before += y;
   }
-  if (lane_id() == 31) sums[warp_id()] = before;
+  w_max = __reduce_max_sync(0xffffffffu, w_max);
+  if (lane_id() == 31) {
+    sums[warp_id()] = before;
+    sums[kThreads / 32 + warp_id()] = w_max;
+  }
   before -= sum;
   if (tid == 0) {
     sh.item = items;
-    sh.off = sh.left = 0;
+    sh.off = sh.left = sh.whole = 0;
     sh.start = 0;
   }
   __syncthreads();
@@ -99,12 +108,21 @@ __device__ __forceinline__ void find_share(Share& sh, long long* sums, int items
   for (int w = 0; w < kThreads / 32; ++w) {
     if (w == warp_id()) before += total;
     total += sums[w];
+    w_max = max(w_max, static_cast<int>(sums[kThreads / 32 + w]));
   }
   const int parts = static_cast<int>(
       max(1ll, min(static_cast<long long>(parts_max), total / min_share)));
   if (tid == 0) {
     sh.total = total;
     sh.parts = parts;
+  }
+  if (static_cast<long long>((items + parts_max - 1) / parts_max) * w_max <=
+      total / parts + cut_cost && cut_cost > 0) {
+    if (tid == 0) {
+      sh.item = c;
+      sh.whole = 1;
+    }
+    return;
   }
   if (c >= parts) return;
   const long long w0 = share_begin(total, parts, c), w1 = share_begin(total, parts, c + 1);
