@@ -114,7 +114,12 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
+    if stream is None and _raw_stream is not None:      # the same handle, without a Stream object
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
     s = torch.cuda.current_stream() if stream is None else stream
     return ctypes.c_void_p(s.cuda_stream)
 
@@ -446,21 +451,48 @@ def dense_causal_mla_decode_paged(q, kv_pool, block_table, seq_len, sm_scale, ou
     return out, lse
 
 
-def _shaped(t, dtype, *shape):
-    """`t` on the current device, contiguous, of that type and shape (-1: any extent)."""
-    t = _dev(t, dtype)
-    if t.device.index != torch.cuda.current_device():
+def _fit(t, dtype, *shape):
+    """Refuses `t` unless it is a contiguous device tensor of that type and shape."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        _dev(t, dtype)
+        raise ValueError(f"expected shape {list(shape)}, got {list(t.shape)}")
+
+
+def _here(t):
+    """Refuses `t` unless it is on the current device, where the library launches."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
         raise ValueError(f"tensor is on {t.device}, the current device is "
                          f"cuda:{torch.cuda.current_device()}")
-    if t.dim() != len(shape) or any(e not in (-1, n) for n, e in zip(t.shape, shape)):
-        raise ValueError(f"expected shape {list(shape)} (-1: any), got {list(t.shape)}")
-    return t
+
+
+def _rank(t, n):
+    if t.dim() != n:
+        raise ValueError(f"expected {n} dimensions, got shape {list(t.shape)}")
+    return t.shape
 
 
 def _paged_cache(kv_pool, block_table, seq_len):
-    _shaped(kv_pool, torch.bfloat16, -1, 64, 576)
-    _shaped(block_table, torch.int32, -1, -1)
-    _shaped(seq_len, torch.int32, block_table.shape[0])
+    """Checks the cache -> (B, max_blocks, nblk)."""
+    B, max_blocks = _rank(block_table, 2)
+    nblk = _rank(kv_pool, 3)[0]
+    _fit(kv_pool, torch.bfloat16, nblk, 64, 576)
+    _fit(block_table, torch.int32, B, max_blocks)
+    _fit(seq_len, torch.int32, B)
+    _here(kv_pool)
+    return B, max_blocks, nblk
+
+
+def _outputs(q, out, lse, *rows):
+    """The attention's outputs, made where not given."""
+    if out is None:
+        out = torch.empty(*rows, 512, dtype=torch.bfloat16, device=q.device)
+    else:
+        _fit(out, torch.bfloat16, *rows, 512)
+    if lse is None:
+        lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+    else:
+        _fit(lse, torch.float32, *rows)
+    return out, lse
 
 
 def split_mla_decode_workspace_size(B, nq, max_blocks, H) -> int:
@@ -469,24 +501,16 @@ def split_mla_decode_workspace_size(B, nq, max_blocks, H) -> int:
 
 def _range_decode(fn, q, kv_pool, block_table, seq_len, extra, sm_scale, out, lse, workspace,
                   stream):
-    _paged_cache(kv_pool, block_table, seq_len)
-    B, max_blocks = block_table.shape
-    _shaped(q, torch.bfloat16, B, -1, -1, 576)
-    nq, H = q.shape[1], q.shape[2]
-    dev = q.device
-    if out is None:
-        out = torch.empty(B, nq, H, 512, dtype=torch.bfloat16, device=dev)
-    if lse is None:
-        lse = torch.empty(B, nq, H, dtype=torch.float32, device=dev)
-    _shaped(out, torch.bfloat16, B, nq, H, 512)
-    _shaped(lse, torch.float32, B, nq, H)
+    B, max_blocks, nblk = _paged_cache(kv_pool, block_table, seq_len)
+    _, nq, H, _ = _rank(q, 4)
+    _fit(q, torch.bfloat16, B, nq, H, 576)
+    out, lse = _outputs(q, out, lse, B, nq, H)
     if workspace is None:
         need = split_mla_decode_workspace_size(B, nq, max_blocks, H)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     _check(getattr(_lib, fn)(_p(q), _p(kv_pool), _p(block_table), _p(seq_len), B, nq, max_blocks,
-                             kv_pool.shape[0], H, *extra, float(sm_scale), _p(out), _p(lse),
-                             _p(_dev(workspace)), workspace.numel() * workspace.element_size(),
-                             _stream(stream)), fn)
+                             nblk, H, *extra, float(sm_scale), _p(out), _p(lse),
+                             _p(_dev(workspace)), workspace.nbytes, _stream(stream)), fn)
     return out, lse
 
 
@@ -514,38 +538,33 @@ def window_mla(q, kv, sinks, window, sm_scale, q_pos0=0, out=None, lse=None, wor
                stream=None):
     """Prefill whose row t sees a window of keys ending at q_pos0 + t and the first
     `sinks` keys -> (out [T][H][512], lse [T][H])."""
-    _shaped(q, torch.bfloat16, -1, -1, 576)
-    _shaped(kv, torch.bfloat16, -1, 576)
-    T, H, S = q.shape[0], q.shape[1], kv.shape[0]
-    if out is None:
-        out = torch.empty(T, H, 512, dtype=torch.bfloat16, device=q.device)
-    if lse is None:
-        lse = torch.empty(T, H, dtype=torch.float32, device=q.device)
-    _shaped(out, torch.bfloat16, T, H, 512)
-    _shaped(lse, torch.float32, T, H)
+    T, H, _ = _rank(q, 3)
+    S = _rank(kv, 2)[0]
+    _fit(q, torch.bfloat16, T, H, 576)
+    _fit(kv, torch.bfloat16, S, 576)
+    _here(q)
+    out, lse = _outputs(q, out, lse, T, H)
     if workspace is None:
         need = window_mla_workspace_size(T, S, H, q_pos0, sinks, window)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     _check(_lib.dsa_window_mla(_p(q), _p(kv), T, S, H, q_pos0, sinks, window, float(sm_scale),
-                               _p(out), _p(lse), _p(_dev(workspace)),
-                               workspace.numel() * workspace.element_size(), _stream(stream)),
-           "dsa_window_mla")
+                               _p(out), _p(lse), _p(_dev(workspace)), workspace.nbytes,
+                               _stream(stream)), "dsa_window_mla")
     return out, lse
 
 
 def attention_mass_paged(q, kv_pool, block_table, seq_len, lse, sm_scale, mass, stream=None):
     """Adds the attention weight the new tokens give to each cached token to its
     running total, in place -> mass [B][ld] (a new token's total starts at 0)."""
-    _paged_cache(kv_pool, block_table, seq_len)
-    B, max_blocks = block_table.shape
-    _shaped(q, torch.bfloat16, B, -1, -1, 576)
-    nq, H = q.shape[1], q.shape[2]
-    _shaped(lse, torch.float32, B, nq, H)
-    _shaped(mass, torch.float32, B, -1)
+    B, max_blocks, nblk = _paged_cache(kv_pool, block_table, seq_len)
+    _, nq, H, _ = _rank(q, 4)
+    _fit(q, torch.bfloat16, B, nq, H, 576)
+    _fit(lse, torch.float32, B, nq, H)
+    ld = _rank(mass, 2)[1]
+    _fit(mass, torch.float32, B, ld)
     _check(_lib.dsa_attention_mass_paged(_p(q), _p(kv_pool), _p(block_table), _p(seq_len), _p(lse),
-                                         B, nq, max_blocks, kv_pool.shape[0], H, float(sm_scale),
-                                         _p(mass), mass.shape[1], _stream(stream)),
-           "dsa_attention_mass_paged")
+                                         B, nq, max_blocks, nblk, H, float(sm_scale), _p(mass), ld,
+                                         _stream(stream)), "dsa_attention_mass_paged")
     return mass
 
 
@@ -555,28 +574,28 @@ def cache_evict_paged(kv_pool, block_table, seq_len, mass, budget, sinks, recent
     `sinks`, the last `recent` and those of the largest totals -> (idx [B][budget],
     the new lengths, the moved totals). `seq_len_out` and `mass_out` may be `seq_len`
     and `mass`; left out, they are new tensors."""
-    _paged_cache(kv_pool, block_table, seq_len)
-    B, max_blocks = block_table.shape
-    nblk, dev = kv_pool.shape[0], kv_pool.device
-    _shaped(mass, torch.float32, B, -1)
+    B, max_blocks, nblk = _paged_cache(kv_pool, block_table, seq_len)
+    ld = _rank(mass, 2)[1]
+    _fit(mass, torch.float32, B, ld)
     if k8_pool is not None:
-        k8_pool = _shaped(_u8(k8_pool), torch.uint8, nblk, 64, 128)
+        k8_pool = _u8(k8_pool)
+        _fit(k8_pool, torch.uint8, nblk, 64, 128)
     if k_scale_pool is not None:
-        _shaped(k_scale_pool, torch.float32, nblk, 64)
+        _fit(k_scale_pool, torch.float32, nblk, 64)
     if idx is None:
-        idx = torch.empty(B, max(budget, 0), dtype=torch.int32, device=dev)
+        idx = torch.empty(B, max(budget, 0), dtype=torch.int32, device=kv_pool.device)
     if seq_len_out is None:
         seq_len_out = torch.empty_like(seq_len)
     if mass_out is None:
         mass_out = torch.zeros_like(mass)
-    _shaped(idx, torch.int32, B, budget)
-    _shaped(seq_len_out, torch.int32, B)
-    _shaped(mass_out, torch.float32, B, -1)
+    ld_out = _rank(mass_out, 2)[1]
+    _fit(idx, torch.int32, B, max(budget, 0))
+    _fit(seq_len_out, torch.int32, B)
+    _fit(mass_out, torch.float32, B, ld_out)
     _check(_lib.dsa_cache_evict_paged(_p(kv_pool), _p(k8_pool), _p(k_scale_pool), _p(block_table),
-                                      _p(seq_len), _p(mass), mass.shape[1], B, max_blocks, nblk,
-                                      budget, sinks, recent, _p(idx), _p(seq_len_out),
-                                      _p(mass_out), mass_out.shape[1], _stream(stream)),
-           "dsa_cache_evict_paged")
+                                      _p(seq_len), _p(mass), ld, B, max_blocks, nblk, budget,
+                                      sinks, recent, _p(idx), _p(seq_len_out), _p(mass_out),
+                                      ld_out, _stream(stream)), "dsa_cache_evict_paged")
     return idx, seq_len_out, mass_out
 
 

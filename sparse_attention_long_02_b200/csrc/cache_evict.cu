@@ -17,9 +17,11 @@
 // evict_move_kernel: a row's destination is never behind its source slot, so a
 // CTA that walks the kept rows in order, reading a step's rows before it writes
 // them, never overwrites a row it has still to read (nor one of the next step,
-// which it reads ahead). The bytes of a row are split over CTAs by column, each
-// moving its columns of every row: no CTA reads what another one writes. Bound
-// by HBM, each moved byte read and written once.
+// which it reads ahead). The bytes of a row are split by column, each slice of
+// columns moved by CTAs of its own: none reads what another slice's write. A
+// slice's rows are split over a cluster of CTAs where there are few sequences;
+// the cluster's barrier then stands between a step's reads and its writes.
+// Bound by HBM, each moved byte read and written once.
 #include "common.cuh"
 #include "dsa_internal.h"
 
@@ -29,8 +31,12 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 40960;                 // keys a CTA keeps in shared memory
-constexpr int kMoveThreads = 512;
-constexpr int kMoveRows = 4;                    // rows a thread moves in one step
+// CTAs of 512 threads and four rows a thread and step where few sequences leave
+// latency to hide; of 256 and two, more of them on an SM and a shorter last
+// wave, for many (64 x 32768 -> 16384: 557 us; 627 us with the former).
+constexpr int kFewThreads = 512, kFewRows = 4;
+constexpr int kManyThreads = 256, kManyRows = 2;
+constexpr int kMoveWant = 2 * 148;              // CTAs a move should have, in clusters of up to 8
 
 // Order-preserving key of a total; NaN below everything, -0 equal to +0.
 __device__ __forceinline__ unsigned total_key(float v) {
@@ -93,8 +99,11 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   const int base = rank * kSelWarps * seg, end = min(n, base + kSelWarps * seg);
   const bool in_smem = kSelWarps * seg <= kSelKeys;
   auto key = [&](int i) { return in_smem ? kept_keys[i - base] : total_key(__ldg(mass + i)); };
-  if (in_smem)
-    for (int i = base + tid; i < end; i += kSelThreads) kept_keys[i - base] = total_key(mass[i]);
+  if (in_smem) {
+#pragma unroll 8
+    for (int i = base + tid; i < end; i += kSelThreads)
+      kept_keys[i - base] = total_key(__ldg(mass + i));
+  }
   // threshold: the want-th largest key of the candidates; `ties` of the keys
   // equal to it are kept
   unsigned thr = 0xffffffffu;
@@ -119,10 +128,17 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
       cluster_sync();
       // this thread's two digits, from the top: 2047 - 2 tid and the one below
       unsigned c0 = 0, c1 = 0;
-      for (int r = 0; r < cl; ++r) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (r >= cl) continue;
         const uint32_t at = mapa(smem_u32(&sm.hist[0][2046 - 2 * tid]), r);
-        c1 += ld_cluster(at);
-        c0 += ld_cluster(at + 4);
+        uint32_t lo2, hi2;
+        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                     : "=r"(lo2), "=r"(hi2)
+                     : "r"(at)
+                     : "memory");
+        c1 += lo2;
+        c0 += hi2;
       }
       unsigned x = c0 + c1;
 #pragma unroll
@@ -210,14 +226,16 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
 }
 
 // One column slice of one sequence: `cols` elements from element `first` of
-// every row (rows of `pitch` elements), kMoveRows * threads / cols rows a step.
-// The next step's rows are on their way while a step's are written.
-template <typename V>
+// every row (rows of `pitch` elements), kMoveRows * threads / cols rows a CTA
+// and step. The next step's rows are on their way while a step's are written.
+template <int kMoveThreads, int kMoveRows, typename V>
 __device__ __forceinline__ void move_columns(const EvictArgs& A, int b, int count, const V* from,
                                              V* to, bool paged, int pitch, int cols, int first) {
-  const int per = kMoveThreads / cols;          // rows of one sub-step
+  const int cl = static_cast<int>(cluster_size());
+  const int per = kMoveThreads / cols * cl;     // the cluster's rows of one sub-step
   const int col = first + static_cast<int>(threadIdx.x) % cols;
-  const int sub = static_cast<int>(threadIdx.x) / cols;
+  const int sub = kMoveThreads / cols * static_cast<int>(cluster_rank()) +
+                  static_cast<int>(threadIdx.x) / cols;
   const int* idx = A.idx + static_cast<long long>(b) * A.budget;
   const int* table = A.block_table + static_cast<long long>(b) * A.max_blocks;
   auto row = [&](int s) -> long long {
@@ -256,7 +274,11 @@ __device__ __forceinline__ void move_columns(const EvictArgs& A, int b, int coun
       load(j0 + step, v[1]);
     else
       load(j0 + step, v[0]);
-    __syncthreads();                            // the step's rows are read
+    // the step's rows are read
+    if (cl > 1)
+      cluster_sync();
+    else
+      __syncthreads();
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
       const int j = j0 + u * per + sub;
@@ -271,24 +293,24 @@ __device__ __forceinline__ void move_columns(const EvictArgs& A, int b, int coun
 }
 
 // kCols: 16-byte columns of a slice (divides 8 and 72).
-template <int kCols>
+template <int kCols, int kMoveThreads, int kMoveRows>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs A) {
   const int b = static_cast<int>(blockIdx.y);
   if (__syncthreads_or(launch_aborted(A.err))) return;
   const int count = A.seq_len_out[b];
   constexpr int kKv = 72 / kCols, kK8 = 8 / kCols;
-  int s = static_cast<int>(blockIdx.x);
+  int s = static_cast<int>(blockIdx.x / cluster_size());
   if (s < kKv) {
     uint4* p = static_cast<uint4*>(A.kv_pool);
-    move_columns<uint4>(A, b, count, p, p, true, 72, kCols, kCols * s);
+    move_columns<kMoveThreads, kMoveRows, uint4>(A, b, count, p, p, true, 72, kCols, kCols * s);
   } else if ((s -= kKv) < kK8) {
     uint4* p = static_cast<uint4*>(A.k8_pool);
-    if (p) move_columns<uint4>(A, b, count, p, p, true, 8, kCols, kCols * s);
+    if (p) move_columns<kMoveThreads, kMoveRows, uint4>(A, b, count, p, p, true, 8, kCols, kCols * s);
   } else if (s == kK8) {
     if (A.k_scale_pool)
-      move_columns<float>(A, b, count, A.k_scale_pool, A.k_scale_pool, true, 1, 1, 0);
+      move_columns<kMoveThreads, kMoveRows, float>(A, b, count, A.k_scale_pool, A.k_scale_pool, true, 1, 1, 0);
   } else if (A.mass_out) {
-    move_columns<float>(A, b, count, A.mass + b * A.ld, A.mass_out + b * A.ld_out, false, 1, 1, 0);
+    move_columns<kMoveThreads, kMoveRows, float>(A, b, count, A.mass + b * A.ld, A.mass_out + b * A.ld_out, false, 1, 1, 0);
   }
 }
 
@@ -316,18 +338,23 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
   if (e != cudaSuccess) return e;
-  // Slices as wide as leaves two CTAs an SM: 128-byte columns move whole lines,
-  // 16-byte ones give a single sequence 82 CTAs.
-  const int want = 2 * 148;
-  if (a.B * 12 >= want)
-    evict_move_kernel<8><<<dim3(12, a.B), kMoveThreads, 0, st>>>(a);
-  else if (a.B * 22 >= want)
-    evict_move_kernel<4><<<dim3(22, a.B), kMoveThreads, 0, st>>>(a);
-  else if (a.B * 42 >= want)
-    evict_move_kernel<2><<<dim3(42, a.B), kMoveThreads, 0, st>>>(a);
-  else
-    evict_move_kernel<1><<<dim3(82, a.B), kMoveThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  // 128-byte slices (whole lines), in clusters as large as leave two CTAs an SM
+  // or so; a few sequences get 64-byte slices too
+  constexpr int kWide = 9 + 1 + 2, kNarrow = 18 + 2 + 2;
+  const bool many = a.B * kWide >= 2 * kMoveWant;
+  const bool narrow = a.B * kWide * 8 < kMoveWant;
+  const int slices = narrow ? kNarrow : kWide;
+  cl = 1;
+  while (cl < 8 && a.B * slices * cl * 2 <= kMoveWant) cl *= 2;
+  cfg.gridDim = dim3(static_cast<unsigned>(slices * cl), static_cast<unsigned>(a.B));
+  cfg.blockDim = dim3(many ? kManyThreads : kFewThreads);
+  cfg.dynamicSmemBytes = 0;
+  at.val.clusterDim.x = static_cast<unsigned>(cl);
+  return cudaLaunchKernelEx(&cfg,
+                            many     ? evict_move_kernel<8, kManyThreads, kManyRows>
+                            : narrow ? evict_move_kernel<4, kFewThreads, kFewRows>
+                                     : evict_move_kernel<8, kFewThreads, kFewRows>,
+                            a);
 }
 
 }  // namespace dsa

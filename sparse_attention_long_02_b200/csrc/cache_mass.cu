@@ -17,7 +17,9 @@
 //
 // Bound by HBM: 1152 bytes and 8 of the total a key; the tensor cores take 36
 // MMAs of 64 cycles a 128-key tile, the exponentials 1024 cycles, an SM's share
-// of the copy bandwidth about 6000.
+// of the copy bandwidth about 6000. (Asking L2 for tiles ahead of their loads
+// made it slower, whatever the instruction: 64 x 32768 tokens 413 us without,
+// 559 us one tile ahead, 700 us three ahead.)
 #include <algorithm>
 
 #include "common.cuh"
@@ -32,7 +34,6 @@ constexpr int kChunk = 128 * 128;               // 128 keys (or rows) x 64 dims
 constexpr int kUnit = 64 * 128;
 // Even, so that each of the two loading warps has its own places.
 constexpr int kRing = 4;
-constexpr int kAhead = 2;                       // tiles of L2 prefetch
 constexpr int kCtas = 148;                      // one an SM
 constexpr int kMinShare = 1;
 
@@ -131,14 +132,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       while (ok && walk.next(A)) {
         const int* table = A.block_table + static_cast<long long>(walk.b) * A.max_blocks;
         const int units = (walk.len + 63) >> 6;
-        auto unit_row = [&](int u) {
-          if (u >= units) return A.kv_rows;
-          const int pb = __ldg(table + u);
-          return pb < 0 || pb >= A.nblk ? A.kv_rows : pb * 64;
-        };
-        auto prefetch = [&](int row) {
-          if (row < A.kv_rows) prefetch_l2(A.kv + static_cast<long long>(row) * 576, 64 * 1152);
-        };
+        auto entry = [&](int u) { return u < units ? __ldg(table + u) : -1; };
+        auto row_of = [&](int e) { return e < 0 || e >= A.nblk ? A.kv_rows : e * 64; };
         for (int rt = 0; ok && rt < A.per_seq; ++rt, ++passes) {
           if (par == 0) {
             if (passes > 0 && !(ok = wait1(sm.q_free, (passes - 1) & 1, abort_flag, err))) break;
@@ -147,23 +142,12 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             for (int a = 0; a < 9; ++a)
               tma_load_2d(smem_u32(sm.q[a]), &tm_q, smem_u32(&sm.q_full), 64 * a, q_row);
           }
-          const int u_end = min(2 * walk.t1, units);
-          auto ahead = [&](int u) { return u < u_end ? unit_row(u) : A.kv_rows; };
-          if (par == 1)
-            for (int u = 2 * walk.t0 + 2; u < 2 * (walk.t0 + kAhead); ++u) prefetch(ahead(u));
-          int r0 = unit_row(2 * walk.t0), r1 = unit_row(2 * walk.t0 + 1);
-          int f0 = ahead(2 * (walk.t0 + kAhead)), f1 = ahead(2 * (walk.t0 + kAhead) + 1);
+          int e0 = entry(2 * walk.t0), e1 = entry(2 * walk.t0 + 1);
           for (int t = walk.t0; ok && t < walk.t1; ++t) {
-            const int c0 = r0, c1 = r1, d0 = f0, d1 = f1;
             // table entries are loaded a tile before they are used
-            r0 = unit_row(2 * t + 2);
-            r1 = unit_row(2 * t + 3);
-            f0 = ahead(2 * (t + 1 + kAhead));
-            f1 = ahead(2 * (t + 1 + kAhead) + 1);
-            if (par == 1) {
-              prefetch(d0);
-              prefetch(d1);
-            }
+            const int c0 = row_of(e0), c1 = row_of(e1);
+            e0 = entry(2 * t + 2);
+            e1 = entry(2 * t + 3);
 #pragma unroll 1
             for (int ch = 0; ch < 9; ++ch, ++ent) {
               if ((ent & 1) != par) continue;

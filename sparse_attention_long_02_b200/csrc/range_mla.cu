@@ -59,7 +59,7 @@ constexpr uint32_t kColQ = 256;                 // after two buffers of 128 logi
 constexpr int kPieces = 8;                      // pieces written down at a time
 constexpr int kPSlots = 4;
 constexpr int kVRing = 4;
-constexpr int kAhead = 2;                       // tiles of L2 prefetch, ahead of CTA 1's V
+constexpr int kAhead = 1;                       // tiles of L2 prefetch, ahead of CTA 1's V
 constexpr float kRebase = 8.0f;                 // lazy rescale threshold (log2 units)
 constexpr int kMaxClusters = 74;                // two CTAs on each of 148 SMs
 constexpr int kScanItems = 16384;               // row tiles a cluster scans for its share
@@ -67,7 +67,7 @@ constexpr int kItemCost = 3;                    // a row tile's fixed cost, in t
 constexpr int kMinShare = 2;                    // tiles (and fixed costs) a cluster takes at least
 // What cutting row tiles costs, in tiles: where there are fewer of them than
 // clusters a cluster writes one part, else two.
-constexpr int kCutCostFew = 3, kCutCostMany = 7;
+constexpr int kCutCostFew = 5, kCutCostMany = 7;
 
 struct LogitsSmem {                             // CTA 0
   uint8_t ring[kRing][kEntry];                  // K, and Q on its way to TMEM
@@ -811,12 +811,13 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
       }
-    } else if (warp == 12) {
+    } else if (warp == 12 && A.block_table) {
       // ------------------------------------------- L2 prefetch (CTA 1)
-      // A tile's cache lines are asked for kAhead tiles before CTA 1 loads its
-      // V (CTA 0 is about two tiles ahead of that). One warp's plain prefetches:
-      // bulk ones go through the TMA engine, whose time CTA 1 needs for V
-      // (64 x 32768: 731 us with them, 635 us with none).
+      // Of a paged cache, whose tiles come from HBM: a tile's cache lines are
+      // asked for kAhead tiles before CTA 1 loads its V. One warp's plain
+      // prefetches (bulk ones take the TMA engine's time). 64 x 32768: 606 us so,
+      // 640 us with none, 774 us six tiles ahead. A prefill finds its window in
+      // L2 already and is slower with them (8191 rows 2.77 -> 2.97 ms).
       // (It may fall behind, so it works out the pieces by itself.)
       volatile int* progress = &ctl.progress;
       int tc = 0;
