@@ -297,6 +297,54 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const int cluster = static_cast<int>(blockIdx.x >> 1);
   const int warp = warp_id(), lane = lane_id();
 
+  // The barriers and the tensor memory are made ready while the share is found;
+  // the other CTA's are known to be by the end of that.
+  if (warp == 15) {
+    auto init = [](unsigned long long& b, int count) { mbar_init(smem_u32(&b), count); };
+    const int i = lane & 7;
+    if (lane < 4) {
+      init(ctl.q_ready[i], 4);
+      init(ctl.k_full[i], 1);
+      init(ctl.k_empty[i], 1);
+      init(ctl.mx_bar[i], 2);
+      init(ctl.p_own[i >> 1][i & 1], 4);
+      init(ctl.p_ack[i >> 1][i & 1], 1);
+      init(ctl.p_room[i], 1);
+      init(ctl.v_full[i], 1);
+      init(ctl.v_empty[i], 1);
+      init(ctl.p_full[i], 1);
+      init(ctl.p_free[i], 1);
+      init(ctl.al_full[i], 1);
+      init(ctl.o_ok[i], 8);
+      init(ctl.pv_done[i], 1);
+      // CTA 1 expects the first atoms of P before CTA 0 can send one
+      if (rank == 1) {
+        mbar_expect_tx(smem_u32(&ctl.p_full[i]), kAtom);
+        mbar_expect_tx(smem_u32(&ctl.al_full[i]), 512);
+      }
+    } else if (lane >= 8 && lane < 16) {
+      init(ctl.piece_full[i], 1);
+      init(ctl.piece_done[i], 1);
+    } else if (lane == 16 || lane == 17) {
+      init(ctl.s_full[i], 1);
+      init(ctl.s_empty[i], 8);
+      init(ctl.clean[i], 8);
+    } else if (lane == 18) {
+      init(ctl.q_free, 1);
+      init(ctl.rope_full, 1);
+      init(ctl.ml_free, 8);
+      init(ctl.o_done, 1);
+      init(ctl.ml_full, 8);
+      ctl.abort_flag = launch_aborted(err) ? 1 : 0;
+      ctl.progress = 0;
+    }
+    fence_barrier_init();
+  } else if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl.tmem_base), 512);
+    tmem_relinquish();
+  }
+  __syncwarp();
+  cluster_arrive();
   if (A.whole) {
     if (threadIdx.x == 0) {
       ctl.share = Share{};
@@ -314,67 +362,28 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                            return item_geom(A, i).tiles + kItemCost;
                          });
   }
-  if (threadIdx.x == 0) {
-    auto init = [](unsigned long long& b, int count) { mbar_init(smem_u32(&b), count); };
-    init(ctl.q_free, 1);
-    init(ctl.rope_full, 1);
-    for (int i = 0; i < 4; ++i) {
-      init(ctl.q_ready[i], 4);
-      init(ctl.k_full[i], 1);
-      init(ctl.k_empty[i], 1);
-      init(ctl.mx_bar[i], 2);
-      init(ctl.p_own[i >> 1][i & 1], 4);
-      init(ctl.p_ack[i >> 1][i & 1], 1);
-      init(ctl.p_room[i], 1);
-      init(ctl.v_full[i], 1);
-      init(ctl.v_empty[i], 1);
-      init(ctl.p_full[i], 1);
-      init(ctl.p_free[i], 1);
-      init(ctl.al_full[i], 1);
-      init(ctl.o_ok[i], 8);
-      init(ctl.pv_done[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      init(ctl.s_full[i], 1);
-      init(ctl.s_empty[i], 8);
-    }
-    for (int i = 0; i < kPieces; ++i) {
-      init(ctl.piece_full[i], 1);
-      init(ctl.piece_done[i], 1);
-    }
-    init(ctl.ml_free, 8);
-    init(ctl.o_done, 1);
-    init(ctl.clean[0], 8);
-    init(ctl.clean[1], 8);
-    init(ctl.ml_full, 8);
-    ctl.abort_flag = launch_aborted(err) ? 1 : 0;
-    ctl.progress = 0;
-    fence_barrier_init();
-    // CTA 1 expects the first atoms of P before CTA 0 can send one
-    if (rank == 1)
-      for (int i = 0; i < 4; ++i) {
-        mbar_expect_tx(smem_u32(&ctl.p_full[i]), kAtom);
-        mbar_expect_tx(smem_u32(&ctl.al_full[i]), 512);
-      }
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&ctl.tmem_base), 512);
-    tmem_relinquish();
-  }
   fence_proxy_async_smem();               // find_share's scratch, before loads land there
   tc_fence_before();
   __syncthreads();
+  tc_fence_after();
+  // each CTA works out the first piece for itself
   Walk walk(ctl.share);
   Piece p;
-  if (rank == 1 && warp == 13) p = walk.next(A);
-  __syncwarp();
-  cluster_sync();          // barriers of both CTAs initialised before any remote arrive
-  tc_fence_after();
+  if (warp == 13) {
+    p = walk.next(A);
+    if (lane == 0) {
+      ctl.piece[0] = p;
+      mbar_arrive(smem_u32(&ctl.piece_full[0]));
+    }
+    __syncwarp();
+  }
+  cluster_wait();
   const uint32_t tmem = ctl.tmem_base;
   volatile int* abort_flag = &ctl.abort_flag;
   bool ok = *abort_flag == 0;
-  // The pieces, written down by CTA 1's warp 13 for every role of both CTAs (the
-  // arithmetic is cold code that each role would wait for between two pieces).
+  // The later pieces are written down by CTA 1's warp 13 for every role of both
+  // CTAs (the arithmetic is cold code that each role would wait for between two
+  // pieces).
   Item& x = p.x;
   int pieces = 0;                               // of this role so far
   auto next_piece = [&](bool whole_warp) {
@@ -849,12 +858,12 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // place it takes was piece k - 8's, which every role has copied by then:
       // no role is more than four atoms of P behind the output, and a piece
       // has at least one.
-      for (;; ++pieces) {
+      for (pieces = 1; p.item >= 0; ++pieces) {
         const int done = pieces - kPieces / 2;
         if (!(ok = ok && (done < 0 || wait32(ctl.piece_done[done & (kPieces - 1)],
                                              (done / kPieces) & 1, abort_flag, err))))
           break;
-        if (pieces > 0) p = walk.next(A);
+        p = walk.next(A);
         const int slot = pieces & (kPieces - 1);
         if (lane == 0) ctl.piece[slot] = p;
         __syncwarp();
@@ -867,7 +876,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           mbar_arrive(smem_u32(&ctl.piece_full[slot]));
           mbar_arrive_remote(mapa(smem_u32(&ctl.piece_full[slot]), peer));
         }
-        if (p.item < 0) break;
       }
     } else if (warp < 12) {
       // ------------------------------------- rescale and output (CTA 1)
