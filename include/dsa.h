@@ -99,6 +99,7 @@ int dsa_get_device_error(dsa_stream_t stream);
  *                            indexer launches inside dsa_forward,
  *                            dsa_forward_fused and dsa_decode_paged)
  *   DSA_DEBUG_STALL_MLA      the sparse MLA (every entry point that runs it)
+ *                            and the split and windowed MLA
  * Synchronises the device. Returns DSA_ERR_INVALID_ARG for unknown bits.
  */
 #define DSA_DEBUG_STALL_INDEXER 1u

@@ -451,18 +451,22 @@ def dense_causal_mla_decode_paged(q, kv_pool, block_table, seq_len, sm_scale, ou
     return out, lse
 
 
-def _fit(t, dtype, *shape):
-    """Refuses `t` unless it is a contiguous device tensor of that type and shape."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+def _fit(t, dev, dtype, *shape):
+    """Refuses `t` unless it is contiguous on device `dev`, of that type and shape."""
+    if (t.dtype != dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous()):
         _dev(t, dtype)
+        if t.get_device() != dev:
+            raise ValueError(f"tensor is on {t.device}, not on cuda:{dev}")
         raise ValueError(f"expected shape {list(shape)}, got {list(t.shape)}")
 
 
 def _here(t):
-    """Refuses `t` unless it is on the current device, where the library launches."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensor is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+    """The index of the current device, where the library launches: `t` must be there."""
+    dev = torch.cuda.current_device() if t.is_cuda else -1
+    if t.get_device() != dev or dev < 0:
+        _dev(t)
+        raise ValueError(f"tensor is on {t.device}, the current device is cuda:{dev}")
+    return dev
 
 
 def _rank(t, n):
@@ -471,27 +475,44 @@ def _rank(t, n):
     return t.shape
 
 
+def _new(stream, make, *args, **kw):
+    """A tensor made by torch in the memory of the stream that will use it."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _scratch(workspace, need, dev, stream):
+    """The caller's workspace, or one for this call; nothing outside the device."""
+    if workspace is None:
+        return _new(stream, torch.empty, max(need(), 256), dtype=torch.uint8, device=dev)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+    return workspace
+
+
 def _paged_cache(kv_pool, block_table, seq_len):
-    """Checks the cache -> (B, max_blocks, nblk)."""
+    """Checks the cache -> (B, max_blocks, nblk, device index)."""
+    dev = _here(kv_pool)
     B, max_blocks = _rank(block_table, 2)
     nblk = _rank(kv_pool, 3)[0]
-    _fit(kv_pool, torch.bfloat16, nblk, 64, 576)
-    _fit(block_table, torch.int32, B, max_blocks)
-    _fit(seq_len, torch.int32, B)
-    _here(kv_pool)
-    return B, max_blocks, nblk
+    _fit(kv_pool, dev, torch.bfloat16, nblk, 64, 576)
+    _fit(block_table, dev, torch.int32, B, max_blocks)
+    _fit(seq_len, dev, torch.int32, B)
+    return B, max_blocks, nblk, dev
 
 
-def _outputs(q, out, lse, *rows):
+def _outputs(dev, stream, out, lse, *rows):
     """The attention's outputs, made where not given."""
     if out is None:
-        out = torch.empty(*rows, 512, dtype=torch.bfloat16, device=q.device)
+        out = _new(stream, torch.empty, *rows, 512, dtype=torch.bfloat16, device=dev)
     else:
-        _fit(out, torch.bfloat16, *rows, 512)
+        _fit(out, dev, torch.bfloat16, *rows, 512)
     if lse is None:
-        lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+        lse = _new(stream, torch.empty, rows, dtype=torch.float32, device=dev)
     else:
-        _fit(lse, torch.float32, *rows)
+        _fit(lse, dev, torch.float32, *rows)
     return out, lse
 
 
@@ -501,16 +522,15 @@ def split_mla_decode_workspace_size(B, nq, max_blocks, H) -> int:
 
 def _range_decode(fn, q, kv_pool, block_table, seq_len, extra, sm_scale, out, lse, workspace,
                   stream):
-    B, max_blocks, nblk = _paged_cache(kv_pool, block_table, seq_len)
+    B, max_blocks, nblk, dev = _paged_cache(kv_pool, block_table, seq_len)
     _, nq, H, _ = _rank(q, 4)
-    _fit(q, torch.bfloat16, B, nq, H, 576)
-    out, lse = _outputs(q, out, lse, B, nq, H)
-    if workspace is None:
-        need = split_mla_decode_workspace_size(B, nq, max_blocks, H)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _fit(q, dev, torch.bfloat16, B, nq, H, 576)
+    out, lse = _outputs(dev, stream, out, lse, B, nq, H)
+    ws = _scratch(workspace, lambda: split_mla_decode_workspace_size(B, nq, max_blocks, H), dev,
+                  stream)
     _check(getattr(_lib, fn)(_p(q), _p(kv_pool), _p(block_table), _p(seq_len), B, nq, max_blocks,
-                             nblk, H, *extra, float(sm_scale), _p(out), _p(lse),
-                             _p(_dev(workspace)), workspace.nbytes, _stream(stream)), fn)
+                             nblk, H, *extra, float(sm_scale), _p(out), _p(lse), _p(ws), ws.nbytes,
+                             _stream(stream)), fn)
     return out, lse
 
 
@@ -538,30 +558,29 @@ def window_mla(q, kv, sinks, window, sm_scale, q_pos0=0, out=None, lse=None, wor
                stream=None):
     """Prefill whose row t sees a window of keys ending at q_pos0 + t and the first
     `sinks` keys -> (out [T][H][512], lse [T][H])."""
+    dev = _here(q)
     T, H, _ = _rank(q, 3)
     S = _rank(kv, 2)[0]
-    _fit(q, torch.bfloat16, T, H, 576)
-    _fit(kv, torch.bfloat16, S, 576)
-    _here(q)
-    out, lse = _outputs(q, out, lse, T, H)
-    if workspace is None:
-        need = window_mla_workspace_size(T, S, H, q_pos0, sinks, window)
-        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _fit(q, dev, torch.bfloat16, T, H, 576)
+    _fit(kv, dev, torch.bfloat16, S, 576)
+    out, lse = _outputs(dev, stream, out, lse, T, H)
+    ws = _scratch(workspace, lambda: window_mla_workspace_size(T, S, H, q_pos0, sinks, window), dev,
+                  stream)
     _check(_lib.dsa_window_mla(_p(q), _p(kv), T, S, H, q_pos0, sinks, window, float(sm_scale),
-                               _p(out), _p(lse), _p(_dev(workspace)), workspace.nbytes,
-                               _stream(stream)), "dsa_window_mla")
+                               _p(out), _p(lse), _p(ws), ws.nbytes, _stream(stream)),
+           "dsa_window_mla")
     return out, lse
 
 
 def attention_mass_paged(q, kv_pool, block_table, seq_len, lse, sm_scale, mass, stream=None):
     """Adds the attention weight the new tokens give to each cached token to its
     running total, in place -> mass [B][ld] (a new token's total starts at 0)."""
-    B, max_blocks, nblk = _paged_cache(kv_pool, block_table, seq_len)
+    B, max_blocks, nblk, dev = _paged_cache(kv_pool, block_table, seq_len)
     _, nq, H, _ = _rank(q, 4)
-    _fit(q, torch.bfloat16, B, nq, H, 576)
-    _fit(lse, torch.float32, B, nq, H)
+    _fit(q, dev, torch.bfloat16, B, nq, H, 576)
+    _fit(lse, dev, torch.float32, B, nq, H)
     ld = _rank(mass, 2)[1]
-    _fit(mass, torch.float32, B, ld)
+    _fit(mass, dev, torch.float32, B, ld)
     _check(_lib.dsa_attention_mass_paged(_p(q), _p(kv_pool), _p(block_table), _p(seq_len), _p(lse),
                                          B, nq, max_blocks, nblk, H, float(sm_scale), _p(mass), ld,
                                          _stream(stream)), "dsa_attention_mass_paged")
@@ -574,24 +593,25 @@ def cache_evict_paged(kv_pool, block_table, seq_len, mass, budget, sinks, recent
     `sinks`, the last `recent` and those of the largest totals -> (idx [B][budget],
     the new lengths, the moved totals). `seq_len_out` and `mass_out` may be `seq_len`
     and `mass`; left out, they are new tensors."""
-    B, max_blocks, nblk = _paged_cache(kv_pool, block_table, seq_len)
+    B, max_blocks, nblk, dev = _paged_cache(kv_pool, block_table, seq_len)
     ld = _rank(mass, 2)[1]
-    _fit(mass, torch.float32, B, ld)
+    _fit(mass, dev, torch.float32, B, ld)
     if k8_pool is not None:
         k8_pool = _u8(k8_pool)
-        _fit(k8_pool, torch.uint8, nblk, 64, 128)
+        _fit(k8_pool, dev, torch.uint8, nblk, 64, 128)
     if k_scale_pool is not None:
-        _fit(k_scale_pool, torch.float32, nblk, 64)
+        _fit(k_scale_pool, dev, torch.float32, nblk, 64)
+    keep = max(budget, 0)
     if idx is None:
-        idx = torch.empty(B, max(budget, 0), dtype=torch.int32, device=kv_pool.device)
+        idx = _new(stream, torch.empty, B, keep, dtype=torch.int32, device=dev)
     if seq_len_out is None:
-        seq_len_out = torch.empty_like(seq_len)
+        seq_len_out = _new(stream, torch.empty_like, seq_len)
     if mass_out is None:
-        mass_out = torch.zeros_like(mass)
+        mass_out = _new(stream, torch.zeros_like, mass)
     ld_out = _rank(mass_out, 2)[1]
-    _fit(idx, torch.int32, B, max(budget, 0))
-    _fit(seq_len_out, torch.int32, B)
-    _fit(mass_out, torch.float32, B, ld_out)
+    _fit(idx, dev, torch.int32, B, keep)
+    _fit(seq_len_out, dev, torch.int32, B)
+    _fit(mass_out, dev, torch.float32, B, ld_out)
     _check(_lib.dsa_cache_evict_paged(_p(kv_pool), _p(k8_pool), _p(k_scale_pool), _p(block_table),
                                       _p(seq_len), _p(mass), ld, B, max_blocks, nblk, budget,
                                       sinks, recent, _p(idx), _p(seq_len_out), _p(mass_out),

@@ -60,7 +60,8 @@ __device__ __forceinline__ int seq_tokens(const MassArgs& A, int b) {
 
 // A CTA's share, a piece (128-key tiles [t0, t1) of a sequence) after another.
 struct MassWalk {
-  int item, off, left;
+  int item, off;
+  long long left;
   int b, len, t0, t1;                           // the piece
   __device__ __forceinline__ explicit MassWalk(const Share& s)
       : item(s.item), off(s.off), left(s.left) {}
@@ -68,7 +69,7 @@ struct MassWalk {
     while (left > 0 && item < A.B) {
       len = seq_tokens(A, item);
       const int tiles = (len + 127) >> 7;
-      const int take = min(tiles - off, left);
+      const int take = static_cast<int>(min(static_cast<long long>(tiles - off), left));
       b = item++;
       t0 = off;
       t1 = off + take;
@@ -127,7 +128,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // ------------------------------------------------------ Q and K loads
     const int par = warp >> 1;
     if (lane == 0) {
-      int ent = 0, passes = 0;
+      int ent = 0, passes = 0, q_loads = 0;
       const uint32_t q_bytes = 9u * static_cast<uint32_t>(A.box_rows) * 128u;
       while (ok && walk.next(A)) {
         const int* table = A.block_table + static_cast<long long>(walk.b) * A.max_blocks;
@@ -141,6 +142,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             mbar_expect_tx(smem_u32(&sm.q_full), q_bytes);
             for (int a = 0; a < 9; ++a)
               tma_load_2d(smem_u32(sm.q[a]), &tm_q, smem_u32(&sm.q_full), 64 * a, q_row);
+            ++q_loads;
           }
           int e0 = entry(2 * walk.t0), e1 = entry(2 * walk.t0 + 1);
           for (int t = walk.t0; ok && t < walk.t1; ++t) {
@@ -166,7 +168,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       if (!ok) {             // let the loads in flight land before this CTA leaves
         for (int c = max(0, ent - kRing); c < ent; ++c)
           if ((c & 1) == par) mbar_drain(smem_u32(&sm.k_full[c & (kRing - 1)]), (c / kRing) & 1);
-        if (par == 0) mbar_drain(smem_u32(&sm.q_full), passes & 1);
+        if (q_loads > 0) mbar_drain(smem_u32(&sm.q_full), (q_loads - 1) & 1);
       }
     }
   } else if (warp == 1) {

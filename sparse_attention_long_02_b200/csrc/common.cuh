@@ -232,11 +232,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
-// Asks for `bytes` (a multiple of 16, 16-byte aligned) of global memory to be
-// brought into L2.
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
 // True in one lane (always the same) of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;

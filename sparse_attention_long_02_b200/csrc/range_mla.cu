@@ -26,9 +26,11 @@
 //   CTA 1: V chunks (64 keys x 256 dims) stream through their own ring;
 //     O (+)= P V (M = 128, N = 256 twice, K = 64); eight warps rescale O in
 //     TMEM when a reference maximum moved, and write the result.
-// Nothing below fp32 crosses but P, which the PV product takes in bf16. Both
-// K and V stream from L2 (each 64-key unit is prefetched a few tiles ahead),
-// so neither role waits for the other's loads.
+// Nothing below fp32 crosses but P, which the PV product takes in bf16. Each
+// role streams its own operand, K from HBM and V, the same rows two tiles later,
+// from L2. (Asking L2 for tiles ahead of the loads does not pay: its lines are
+// lost again before they are used; 64 x 32768 tokens read 797 MB for 456 when it
+// ran six tiles ahead.)
 //
 // Work split. The tiles of all row tiles form one list; each cluster takes an
 // equal share of it, wherever it begins and ends (or whole row tiles in turn,
@@ -59,7 +61,6 @@ constexpr uint32_t kColQ = 256;                 // after two buffers of 128 logi
 constexpr int kPieces = 8;                      // pieces written down at a time
 constexpr int kPSlots = 4;
 constexpr int kVRing = 4;
-constexpr int kAhead = 1;                       // tiles of L2 prefetch, ahead of CTA 1's V
 constexpr float kRebase = 8.0f;                 // lazy rescale threshold (log2 units)
 constexpr int kMaxClusters = 74;                // two CTAs on each of 148 SMs
 constexpr int kScanItems = 16384;               // row tiles a cluster scans for its share
@@ -191,10 +192,10 @@ struct Piece {
 static_assert(sizeof(Piece) % 4 == 0 && sizeof(Piece) <= 128, "at most a word a lane");
 
 struct Walk {
-  int item, off, left, whole;
-  long long start;
+  int item, off, whole;
+  long long left, start;
   __device__ __forceinline__ explicit Walk(const Share& s)
-      : item(s.item), off(s.off), left(s.left), whole(s.whole), start(s.start) {}
+      : item(s.item), off(s.off), whole(s.whole), left(s.left), start(s.start) {}
   __device__ __forceinline__ Piece next(const RangeArgs& A) {
     Piece p;
     p.item = -1;
@@ -213,7 +214,7 @@ struct Walk {
     while (left > 0 && item < A.items) {
       p.x = item_geom(A, item);
       const int weight = p.x.tiles + kItemCost;
-      const int take = min(weight - off, left);
+      const int take = static_cast<int>(min(static_cast<long long>(weight - off), left));
       p.t0 = max(0, off - kItemCost);
       p.t1 = off + take - kItemCost;
       p.start = start;
@@ -258,7 +259,6 @@ struct Ctl {
   Share share;                                  // of the row tiles' weights
   unsigned long long piece_full[kPieces];
   unsigned long long piece_done[kPieces];       // CTA 1: the piece's output is on its way
-  int progress;                                 // CTA 1: tiles whose V loads have begun
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -336,7 +336,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       init(ctl.o_done, 1);
       init(ctl.ml_full, 8);
       ctl.abort_flag = launch_aborted(err) ? 1 : 0;
-      ctl.progress = 0;
     }
     fence_barrier_init();
   } else if (warp == 1) {
@@ -404,7 +403,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // piece's first tile each K entry follows the Q entry it meets.
       const int par = warp >> 1;
       if (lane == 0) {
-        int ent = 0;
+        int ent = 0, ropes = 0;
         for (; next_piece(false); ++pieces) {
           const int q_row = static_cast<int>(x.row0);
           int e0 = unit_entry(A, x, 2 * p.t0), e1 = unit_entry(A, x, 2 * p.t0 + 1);
@@ -424,6 +423,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                   break;
                 mbar_expect_tx(smem_u32(&ctl.rope_full), kAtom);
                 tma_load_2d(smem_u32(sl.q_rope), &tm_q, smem_u32(&ctl.rope_full), 512, q_row);
+                ++ropes;
               }
               if ((ent & 1) != par) continue;
               const int st = ent & (kRing - 1);
@@ -452,7 +452,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           for (int c = max(0, ent - kRing); c < ent; ++c)
             if ((c & 1) == par)
               mbar_drain(smem_u32(&ctl.k_full[c & (kRing - 1)]), (c / kRing) & 1);
-          if (par == 0) mbar_drain(smem_u32(&ctl.rope_full), pieces & 1);
+          if (ropes > 0) mbar_drain(smem_u32(&ctl.rope_full), (ropes - 1) & 1);
         }
       }
     } else if (warp >= 12) {
@@ -724,8 +724,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // ---------------------------------------------------- V loads (CTA 1)
       if (lane == 0) {
         int vc = 0;
-        volatile int* progress = &ctl.progress;
-        int tc = 0;
         for (; next_piece(false); ++pieces) {
           // table entries are loaded a tile before they are used
           int e0 = unit_entry(A, x, 2 * p.t0), e1 = unit_entry(A, x, 2 * p.t0 + 1);
@@ -734,7 +732,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const int c0 = entry_row(A, e0), c1 = entry_row(A, e1);
             e0 = unit_entry(A, x, 2 * t + 2);
             e1 = unit_entry(A, x, 2 * t + 3);
-            *progress = ++tc;
             for (int h = 0; h < 2 * n; ++h, ++vc) {
               const int st = vc & 3;
               if (vc >= kVRing &&
@@ -817,38 +814,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mbar_arrive_remote(mapa(smem_u32(&ctl.p_room[slot]), peer));
               }
             }
-          }
-        }
-      }
-    } else if (warp == 12 && A.block_table) {
-      // ------------------------------------------- L2 prefetch (CTA 1)
-      // Of a paged cache, whose tiles come from HBM: a tile's cache lines are
-      // asked for kAhead tiles before CTA 1 loads its V. One warp's plain
-      // prefetches (bulk ones take the TMA engine's time). 64 x 32768: 606 us so,
-      // 640 us with none, 774 us six tiles ahead. A prefill finds its window in
-      // L2 already and is slower with them (8191 rows 2.77 -> 2.97 ms).
-      // (It may fall behind, so it works out the pieces by itself.)
-      volatile int* progress = &ctl.progress;
-      int tc = 0;
-      while (ok && (p = walk.next(A)).item >= 0) {
-        {
-          const char* at = reinterpret_cast<const char*>(A.q + x.row0 * 576);
-          for (int i = lane; i < 9 * x.nrows; i += 32)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * i));
-        }
-        for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
-          const unsigned long long t0 = globaltimer();
-          while (*progress + kAhead < tc && ok) {
-            ok = *abort_flag == 0 && globaltimer() - t0 < kWaitLimitNs;
-            __nanosleep(200);
-          }
-          ok = __all_sync(0xffffffffu, ok);
-          for (int u = 2 * t; u < min(2 * t + 2, x.nu); ++u) {
-            const int row = entry_row(A, unit_entry(A, x, u));
-            const int lines = 9 * min(64, A.kv_rows - row);     // of 128 bytes (none: row kv_rows)
-            const char* at = reinterpret_cast<const char*>(A.kv + static_cast<long long>(row) * 576);
-            for (int i = lane; i < lines; i += 32)
-              asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * i));
           }
         }
       }
@@ -1054,8 +1019,12 @@ range_join_kernel(const __grid_constant__ RangeArgs A) {
   __shared__ int2 recs[kMaxClusters];
   const int warp = warp_id(), lane = lane_id();
   const bool skip = launch_aborted(A.err);
-  if (static_cast<int>(threadIdx.x) < A.clusters) recs[threadIdx.x] = A.rec[threadIdx.x];
-  if (__syncthreads_or(skip)) return;
+  bool cut = false;
+  if (static_cast<int>(threadIdx.x) < A.clusters) {
+    recs[threadIdx.x] = A.rec[threadIdx.x];
+    cut = recs[threadIdx.x].x >= 0;
+  }
+  if (!__syncthreads_or(cut) || __syncthreads_or(skip)) return;
   const int row_blocks = (A.rows_pad + 31) >> 5;
   int task = static_cast<int>(blockIdx.x);      // within the records from c on
   for (int c = 0; c < A.clusters; ++c) {

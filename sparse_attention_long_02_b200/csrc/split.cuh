@@ -51,7 +51,8 @@ __device__ __forceinline__ bool wait32(unsigned long long& b, uint32_t parity,
 // laid end to end and cut into equal parts.
 struct Share {
   long long total, start;                       // all weight; the weight before the first item
-  int item, off, left, parts;                   // first item, offset into it, weight of the share
+  long long left;                               // weight of the share
+  int item, off, parts;                         // first item, offset into it
   int whole;                                    // items c, c + parts_max, ... whole instead
 };
 
@@ -100,8 +101,8 @@ __device__ __forceinline__ void find_share(Share& sh, long long* sums, int items
   before -= sum;
   if (tid == 0) {
     sh.item = items;
-    sh.off = sh.left = sh.whole = 0;
-    sh.start = 0;
+    sh.off = sh.whole = 0;
+    sh.left = sh.start = 0;
   }
   __syncthreads();
   long long total = 0;
@@ -133,7 +134,7 @@ __device__ __forceinline__ void find_share(Share& sh, long long* sums, int items
       if (w0 < at + w) {
         sh.item = i;
         sh.off = static_cast<int>(w0 - at);
-        sh.left = static_cast<int>(w1 - w0);
+        sh.left = w1 - w0;
         sh.start = at;
         break;
       }

@@ -607,3 +607,137 @@ def test_decode_totals_eviction_decode(dsa):
                    np.ones((16, m), bool))
         check_rows(wout[b].view(-1, 512), wlse[b].view(-1), q2[b].view(-1, 576), k,
                    sees(m - 1, m, 4, 100)[None].repeat(16, 0))
+
+
+# ------------------------------------------------ streams, faults, workspaces
+
+def test_window_decode_hidden_keys_do_not_matter(dsa):
+    """Keys no query sees hold NaN and infinities, inside blocks that are read."""
+    for nq, H, sinks, window in ((1, 128, 3, 70), (2, 128, 70, 5), (3, 8, 0, 130), (4, 31, 1, 1)):
+        lens = [1000, 777, 130, 65, 3]
+        c = make_cache(lens, 60 + nq)
+        for b, n in enumerate(lens):
+            see = np.stack([sees(n - nq + j, n, sinks, window) for j in range(nq)]).any(0)
+            for s in np.nonzero(~see)[0]:
+                row = c["kv_pool"][int(c["block_table"][b, s // 64]), s % 64]
+                row[:] = (math.nan, math.inf, -math.inf)[s % 3]
+        q = randn(c["g"], len(lens), nq, H, 576)
+        out, lse = dsa.window_mla_decode_paged(q, c["kv_pool"], c["block_table"], c["seq_len"],
+                                               sinks, window, SM)
+        no_device_error(dsa)
+        for b, n in enumerate(lens):
+            k = rows_of(c, b, n)
+            see = np.stack([sees(n - nq + j, n, sinks, window) for j in range(nq)])
+            k[~see.any(0)] = 0.0
+            check_rows(out[b].view(-1, 512), lse[b].view(-1), q[b].view(-1, 576), k,
+                       see.repeat(H, 0))
+
+
+def test_a_timeout_is_reported_and_nothing_runs_until_it_is_read(dsa):
+    """The bounded waits run out (a barrier that nothing arrives at), the call comes
+    back, later kernels leave everything as it is, and the next clean call is right."""
+    lens = [500, 90]
+    c = make_cache(lens, 70, poison=False)
+    q = randn(c["g"], 2, 1, 128, 576)
+    cache = (c["kv_pool"], c["block_table"], c["seq_len"])
+    mass = torch.rand(2, 512, generator=c["g"], device="cuda")
+    lse0 = torch.zeros(2, 1, 128, device="cuda")
+    kv0, mass0 = c["kv_pool"].clone(), mass.clone()
+    no_device_error(dsa)
+    dsa.debug_stall(dsa.DEBUG_STALL_MLA)
+    try:
+        dsa.split_mla_decode_paged(q, *cache, SM)
+        dsa.attention_mass_paged(q, *cache, lse0, SM, mass)
+        idx = torch.full((2, 64), -9, dtype=torch.int32, device="cuda")
+        lens_out = torch.full((2,), -9, dtype=torch.int32, device="cuda")
+        dsa.cache_evict_paged(*cache, mass, 64, 0, 8, idx=idx, seq_len_out=lens_out, mass_out=mass)
+        st = dsa.get_device_error()
+    finally:
+        dsa.debug_stall(0)
+    assert st == -5, dsa.STATUS.get(st, st)
+    assert torch.equal(mass, mass0) and torch.equal(c["kv_pool"], kv0)
+    assert (idx == -9).all() and (lens_out == -9).all()
+    out, lse = dsa.split_mla_decode_paged(q, *cache, SM)
+    no_device_error(dsa)
+    for b, n in enumerate(lens):
+        check_rows(out[b].view(-1, 512), lse[b].view(-1), q[b].view(-1, 576), rows_of(c, b, n),
+                   np.ones((128, n), bool))
+
+
+def test_two_calls_at_once(dsa):
+    """Different problems on two streams, each with a workspace of its own, many times
+    over; and a stream given without a workspace or outputs."""
+    g = torch.Generator(device="cuda").manual_seed(80)
+    c = make_cache([3000, 17, 900], 81, poison=False)
+    qa = randn(g, 3, 2, 128, 576)
+    qb, kvb = randn(g, 500, 16, 576), randn(g, 500, 576)
+    cache = (c["kv_pool"], c["block_table"], c["seq_len"])
+    ra = dsa.split_mla_decode_paged(qa, *cache, SM)
+    rb = dsa.window_mla(qb, kvb, 4, 100, SM)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        got.append((dsa.split_mla_decode_paged(qa, *cache, SM, stream=s1),
+                    dsa.window_mla(qb, kvb, 4, 100, SM, stream=s2)))
+    torch.cuda.synchronize()
+    no_device_error(dsa)
+    for a, b in got:
+        assert torch.equal(a[0], ra[0]) and torch.equal(a[1], ra[1])
+        assert torch.equal(b[0], rb[0]) and torch.equal(b[1], rb[1])
+
+
+def test_workspace_ends_where_it_says(dsa):
+    for B, nq, H, lens in ((1, 1, 128, [5000]), (3, 2, 31, [700, 3, 1500])):
+        c = make_cache(lens, 90 + B, poison=False)
+        q = randn(c["g"], B, nq, H, 576)
+        mb = c["block_table"].shape[1]
+        need = dsa.split_mla_decode_workspace_size(B, nq, mb, H)
+        buf = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+        cache = (c["kv_pool"], c["block_table"], c["seq_len"])
+        a = dsa.split_mla_decode_paged(q, *cache, SM, workspace=buf[:need])
+        assert (buf[need:] == 171).all()
+        b = dsa.split_mla_decode_paged(q, *cache, SM)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        with pytest.raises(dsa.DSAError):
+            dsa.split_mla_decode_paged(q, *cache, SM, workspace=buf[:need - 1])
+    no_device_error(dsa)
+
+
+@pytest.mark.parametrize("T,H,window", [(300, 128, 200), (75, 128, 2000), (149, 128, 65),
+                                        (1200, 16, 500), (20000, 1, 9)])
+def test_window_prefill_shares(dsa, T, H, window):
+    """Row tiles cut over several shares and whole ones, one share holding many."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    p0 = 3000 if T < 100 else 0
+    q, kv = randn(g, T, H, 576), randn(g, p0 + T, 576)
+    out, lse = dsa.window_mla(q, kv, 2, window, SM, q_pos0=p0)
+    no_device_error(dsa)
+    k = kv.double().cpu().numpy()
+    for t in sorted({0, 1, T // 3, T // 2, T - 2, T - 1}):
+        see = sees(p0 + t, p0 + T, 2, window)
+        cols = np.nonzero(see)[0]
+        check_rows(out[t], lse[t], q[t], k[cols], np.ones((H, len(cols)), bool))
+
+
+def test_nothing_to_do(dsa):
+    """Empty batches and prompts, and batches of empty sequences."""
+    kv = torch.zeros(2, 64, 576, dtype=torch.bfloat16, device="cuda")
+    q0 = torch.zeros(0, 1, 8, 576, dtype=torch.bfloat16, device="cuda")
+    t0 = torch.zeros(0, 2, dtype=torch.int32, device="cuda")
+    l0 = torch.zeros(0, dtype=torch.int32, device="cuda")
+    out, lse = dsa.split_mla_decode_paged(q0, kv, t0, l0, SM)
+    assert out.shape == (0, 1, 8, 512) and lse.shape == (0, 1, 8)
+    dsa.window_mla(q0[:, 0], kv[0], 0, 4, SM)
+    dsa.attention_mass_paged(q0, kv, t0, l0, lse, SM, torch.zeros(0, 128, device="cuda"))
+    dsa.cache_evict_paged(kv, t0, l0, torch.zeros(0, 128, device="cuda"), 5, 0, 0)
+    q = torch.ones(90, 2, 8, 576, dtype=torch.bfloat16, device="cuda")
+    t = torch.full((90, 2), -1, dtype=torch.int32, device="cuda")
+    n = torch.zeros(90, dtype=torch.int32, device="cuda")
+    out, lse = dsa.split_mla_decode_paged(q, kv, t, n, SM)
+    assert (out == 0).all() and (lse == -math.inf).all()
+    mass = torch.full((90, 128), 3.0, device="cuda")
+    dsa.attention_mass_paged(q, kv, t, n, lse, SM, mass)
+    idx, new, _ = dsa.cache_evict_paged(kv, t, n, mass, 5, 1, 1)
+    assert (mass == 3).all() and (idx == -1).all() and (new == 0).all()
+    no_device_error(dsa)
