@@ -704,6 +704,25 @@ def test_workspace_ends_where_it_says(dsa):
     no_device_error(dsa)
 
 
+def test_outputs_on_any_16_byte_boundary(dsa):
+    """Outputs and inputs that start 16 bytes into an allocation."""
+    g = torch.Generator(device="cuda").manual_seed(95)
+
+    def off(*shape):
+        n = math.prod(shape)
+        return torch.zeros(n + 8, dtype=torch.bfloat16, device="cuda")[8:].view(*shape)
+
+    T, H, S = 200, 128, 200
+    q, kv, out = off(T, H, 576), off(S, 576), off(T, H, 512)
+    q.copy_(randn(g, T, H, 576))
+    kv.copy_(randn(g, S, 576))
+    ref, ref_lse = dsa.window_mla(q.clone(), kv.clone(), 1, 90, SM)
+    got, lse = dsa.window_mla(q, kv, 1, 90, SM, out=out)
+    no_device_error(dsa)
+    assert got.data_ptr() == out.data_ptr() and out.data_ptr() % 32 == 16
+    assert torch.equal(got, ref) and torch.equal(lse, ref_lse)
+
+
 @pytest.mark.parametrize("T,H,window", [(300, 128, 200), (75, 128, 2000), (149, 128, 65),
                                         (1200, 16, 500), (20000, 1, 9)])
 def test_window_prefill_shares(dsa, T, H, window):
