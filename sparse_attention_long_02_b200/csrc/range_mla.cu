@@ -1005,108 +1005,169 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   }
 }
 
-// Joins the parts of the cut row tiles. A task is 32 rows and 32 value dims of
-// a row tile (8 where it has many parts, which four warps then share); record c
-// names the row tile whose first tile closes cluster c's share. The parts'
-// weights are worked out once a row; then each warp adds up four dims of 32 rows
-// (512 consecutive bytes of a part), eight parts in flight.
-constexpr int kJoinThreads = 256, kJoinCtas = 5 * 148;
+// Joins the parts of the cut row tiles. Record c names the row tile whose first
+// tile closes cluster c's share. A task is 32 rows and 128 value dims of a row
+// tile, 16 dims a warp; where the row tile has many parts, 8 dims, whose parts
+// the eight warps share. The weights are worked out once a task. A warp reads
+// 512 consecutive bytes at a time (four dims of 32 rows), eight reads in
+// flight, the first of them asked for before the weights are known.
+constexpr int kJoinThreads = 256, kJoinResident = 3, kJoinCtas = kJoinResident * 148;
 constexpr int kJoinBatch = (kMaxClusters + 7) / 8;              // parts a warp weighs
-__global__ void __launch_bounds__(kJoinThreads, 5)
-range_join_kernel(const __grid_constant__ RangeArgs A) {
-  __shared__ float weight[kMaxClusters][32], top[8][32], sum[8][32];
-  __shared__ float4 partial[8][32];
-  __shared__ int2 recs[kMaxClusters];
+constexpr int kJoinRecs = (kMaxClusters + 31) / 32;             // records a lane looks at
+constexpr int kJoinMany = 16;
+constexpr int kJoinFewDims = 4, kJoinManyDims = 2;              // a warp's dims, in fours
+struct JoinSmem {
+  float weight[kMaxClusters][32];
+  float top[8][32], sum[8][32];
+  float4 partial[8][kJoinManyDims][32];
+};
+__device__ __forceinline__ int join_tasks(int parts) {          // of 32 rows
+  return parts > kJoinMany ? 128 / kJoinManyDims : 128 / (8 * kJoinFewDims);
+}
+// One task: dims 4 c4 .. 4 (c4 + kDims) of 32 rows for this warp, its parts [i0, i1).
+template <int kDims, bool kShared>
+__device__ __forceinline__ void join_rows(JoinSmem& sj, const RangeArgs& A, long long row, bool valid,
+                                          int r, int c, int n, int c4, int i0, int i1) {
+  constexpr int kStep = 8 / kDims;              // parts at a time
   const int warp = warp_id(), lane = lane_id();
-  const bool skip = launch_aborted(A.err);
-  bool cut = false;
-  if (static_cast<int>(threadIdx.x) < A.clusters) {
-    recs[threadIdx.x] = A.rec[threadIdx.x];
-    cut = recs[threadIdx.x].x >= 0;
+  auto slot = [&](int i) { return static_cast<long long>(2 * (c + i) + (i == 0 ? 1 : 0)); };
+  const long long pitch = 128ll * A.rows_pad;
+  const float4* part = A.part_o + static_cast<long long>(c4) * A.rows_pad + r;
+  float4 v[8];
+  auto fetch = [&](int i) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      v[k] = valid && i + k / kDims < i1
+                 ? part[slot(i + k / kDims) * pitch + (k % kDims) * A.rows_pad]
+                 : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  float2 ml[kJoinBatch];
+#pragma unroll
+  for (int k = 0; k < kJoinBatch; ++k) {
+    const int i = warp + 8 * k;
+    ml[k] = valid && i < n ? A.part_ml[slot(i) * A.rows_pad + r] : make_float2(-INFINITY, 0.f);
   }
-  if (!__syncthreads_or(cut) || __syncthreads_or(skip)) return;
+  fetch(i0);
+  float m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int k = 0; k < kJoinBatch; ++k) m = fmaxf(m, ml[k].x);
+  __syncthreads();                              // the task before is done with the tables
+  sj.top[warp][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, sj.top[w][lane]);
+  const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+  for (int k = 0; k < kJoinBatch; ++k) {
+    const int i = warp + 8 * k;
+    if (i >= n) continue;
+    const float w = fast_exp2(ml[k].x - base);
+    sj.weight[i][lane] = w;
+    l += ml[k].x == -INFINITY ? ml[k].y : w * ml[k].y;          // (a NaN sum of a part stays one)
+  }
+  sj.sum[warp][lane] = l;
+  __syncthreads();
+  float4 o[kDims] = {};
+  auto add = [](float4& s, const float4& a, float w) {
+    s.x += w * a.x;
+    s.y += w * a.y;
+    s.z += w * a.z;
+    s.w += w * a.w;
+  };
+  for (int i = i0; i < i1;) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (i + k / kDims < i1) add(o[k % kDims], v[k], sj.weight[i + k / kDims][lane]);
+    i += kStep;
+    if (i < i1) fetch(i);
+  }
+  if constexpr (kShared) {
+#pragma unroll
+    for (int d = 0; d < kDims; ++d) sj.partial[warp][d][lane] = o[d];
+    __syncthreads();
+    if (warp != 0) return;
+    for (int w = 1; w < 8; ++w) {
+#pragma unroll
+      for (int d = 0; d < kDims; ++d) add(o[d], sj.partial[w][d][lane], 1.f);
+    }
+  }
+  if (!valid) return;
+  l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) l += sj.sum[w][lane];
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t w[2 * kDims];
+#pragma unroll
+  for (int d = 0; d < kDims; ++d) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o[d].x * inv, o[d].y * inv);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(o[d].z * inv, o[d].w * inv);
+    w[2 * d] = *reinterpret_cast<const uint32_t*>(&a);
+    w[2 * d + 1] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  uint4* out = reinterpret_cast<uint4*>(A.out + row * 512 + 4 * c4);
+#pragma unroll
+  for (int d = 0; d < kDims / 2; ++d)
+    out[d] = make_uint4(w[4 * d], w[4 * d + 1], w[4 * d + 2], w[4 * d + 3]);
+  if (c4 == 0 && A.lse)
+    A.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+__global__ void __launch_bounds__(kJoinThreads, kJoinResident)
+range_join_kernel(const __grid_constant__ RangeArgs A) {
+  __shared__ JoinSmem sj;
+  const int warp = warp_id(), lane = lane_id();
   const int row_blocks = (A.rows_pad + 31) >> 5;
-  int task = static_cast<int>(blockIdx.x);      // within the records from c on
-  for (int c = 0; c < A.clusters; ++c) {
-    const int2 rec = recs[c];
-    if (rec.x < 0) continue;
-    const int n = rec.y - c + 1;                // parts: slot 1 of c, slot 0 of c+1 .. rec.y
-    const int ways = n > 16 ? 4 : 1, across = 8 / ways;         // warps on one group of dims, groups
-    const int per_row = 128 / across, per_rec = per_row * row_blocks;
-    if (task >= per_rec) {
-      task -= per_rec;
-      continue;
+  // the records' tasks, laid end to end: this lane's end at `end`
+  int item[kJoinRecs], parts[kJoinRecs], tasks = 0;
+#pragma unroll
+  for (int k = 0; k < kJoinRecs; ++k) {
+    const int c = kJoinRecs * lane + k;
+    const int2 rec = c < A.clusters ? A.rec[c] : make_int2(-1, 0);
+    item[k] = rec.x;
+    parts[k] = rec.y - c + 1;                   // slot 1 of c, slot 0 of c+1 .. rec.y
+  }
+  const bool skip = launch_aborted(A.err);
+#pragma unroll
+  for (int k = 0; k < kJoinRecs; ++k)
+    if (item[k] >= 0) tasks += join_tasks(parts[k]) * row_blocks;
+  int end = tasks;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end += y;
+  }
+  const int total = __shfl_sync(0xffffffffu, end, 31);
+  if (__syncthreads_or(skip)) return;
+  for (int task = static_cast<int>(blockIdx.x); task < total; task += kJoinCtas) {
+    const int owner = __ffs(__ballot_sync(0xffffffffu, task < end)) - 1;
+    int at = task - (end - tasks), c = 0, it = 0, n = 0;
+#pragma unroll
+    for (int k = 0; k < kJoinRecs; ++k) {
+      if (item[k] < 0 || n) continue;
+      const int t = join_tasks(parts[k]) * row_blocks;
+      if (at < t) {
+        c = kJoinRecs * lane + k;
+        it = item[k];
+        n = parts[k];
+      } else {
+        at -= t;
+      }
     }
-    const Item x = item_geom(A, rec.x);
-    auto slot = [&](int i) { return static_cast<long long>(2 * (c + i) + (i == 0 ? 1 : 0)); };
-    for (; task < per_rec; task += kJoinCtas) {
-      const int block = task / per_row, r = 32 * block + lane;
-      const bool valid = r < x.nrows;
-      float2 ml[kJoinBatch];
-#pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k) {
-        const int i = warp + 8 * k;
-        ml[k] = valid && i < n ? A.part_ml[slot(i) * A.rows_pad + r] : make_float2(-INFINITY, 0.f);
-      }
-      float m = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k) m = fmaxf(m, ml[k].x);
-      __syncthreads();                          // the task before is done with the tables
-      top[warp][lane] = m;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < 8; ++w) m = fmaxf(m, top[w][lane]);
-      const float base = m == -INFINITY ? 0.f : m;
-#pragma unroll
-      for (int k = 0; k < kJoinBatch; ++k) {
-        const int i = warp + 8 * k;
-        if (i >= n) continue;
-        const float w = fast_exp2(ml[k].x - base);
-        weight[i][lane] = w;
-        l += ml[k].x == -INFINITY ? ml[k].y : w * ml[k].y;      // (a NaN sum of a part stays one)
-      }
-      sum[warp][lane] = l;
-      __syncthreads();
-      const int c4 = across * (task - block * per_row) + warp % across, way = warp / across;
-      const long long pitch = 128ll * A.rows_pad;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](const float4& v, float w) {
-        o.x += w * v.x;
-        o.y += w * v.y;
-        o.z += w * v.z;
-        o.w += w * v.w;
-      };
-      if (valid) {
-        const float4* part = A.part_o + static_cast<long long>(c4) * A.rows_pad + r;
-        int i = n * way / ways;
-        const int end = n * (way + 1) / ways;
-        for (; i + 8 <= end; i += 8) {
-          float4 v[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) v[k] = part[slot(i + k) * pitch];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) add(v[k], weight[i + k][lane]);
-        }
-        for (; i < end; ++i) add(part[slot(i) * pitch], weight[i][lane]);
-      }
-      if (ways > 1) {
-        partial[warp][lane] = o;
-        __syncthreads();
-        for (int w = 1; w < ways && way == 0; ++w) add(partial[warp + w * across][lane], 1.f);
-      }
-      if (!valid || way != 0) continue;
-      l = 0.f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) l += sum[w][lane];
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-      const __nv_bfloat162 b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-      *reinterpret_cast<uint2*>(A.out + (x.row0 + r) * 512 + 4 * c4) = make_uint2(
-          *reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-      if (c4 == 0 && A.lse)
-        A.lse[x.row0 + r] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-    }
-    task -= per_rec;
+    at = __shfl_sync(0xffffffffu, at, owner);
+    c = __shfl_sync(0xffffffffu, c, owner);
+    it = __shfl_sync(0xffffffffu, it, owner);
+    n = __shfl_sync(0xffffffffu, n, owner);
+    const int b = it / A.per_seq, j0 = (it - b * A.per_seq) * A.G;
+    const int nq = A.block_table ? A.nq : A.T;
+    const int across = join_tasks(n), block = at / across, group = at - block * across;
+    const int r = 32 * block + lane;
+    const bool valid = r < min(A.G, nq - j0) * A.H;
+    const long long row = (static_cast<long long>(b) * nq + j0) * A.H + r;
+    if (n > kJoinMany)
+      join_rows<kJoinManyDims, true>(sj, A, row, valid, r, c, n, kJoinManyDims * group,
+                                     n * warp / 8, n * (warp + 1) / 8);
+    else
+      join_rows<kJoinFewDims, false>(sj, A, row, valid, r, c, n, kJoinFewDims * (8 * group + warp),
+                                     0, n);
   }
 }
 
