@@ -7,8 +7,12 @@
 // the sequence's slots 0 .. budget-1, in place.
 //
 // evict_select_kernel, a cluster of 1 to 8 CTAs per sequence: a radix select
-// (11 + 11 + 10 bits) of the threshold total over histograms that the CTAs add
-// up through distributed shared memory. With `ties` the number of totals equal
+// (11 + 11 + 10 bits) of the threshold total over the CTAs' histograms, of which
+// one warp reads, through distributed shared memory, first the sums of 64 bins
+// and then the 64 bins that matter. It runs each of its instructions a few times
+// only and is bound by latency, that of its own code among them: loops are kept
+// short and rolled (with the keys in registers and the loops over them unrolled
+// 16 times one sequence of 131072 tokens took 74 us instead of 66). With `ties` the number of totals equal
 // to the threshold that are kept, slot i's place is
 //   (kept for certain before i) + min(ties, equal before i),
 // so one counting pass and one writing pass over each warp's own run of slots
@@ -31,6 +35,7 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 40960;                 // keys a CTA keeps in shared memory
+constexpr int kBins = 2048;
 // CTAs of 512 threads and four rows a thread and step where few sequences leave
 // latency to hide; of 256 and two, more of them on an SM and a shorter last
 // wave, for many (64 x 32768 -> 16384: 557 us; 627 us with the former).
@@ -46,10 +51,11 @@ __device__ __forceinline__ unsigned total_key(float v) {
 }
 
 struct SelSmem {
-  unsigned hist[4][2048];                       // by lane % 4; [0] then holds the CTA's sum
+  unsigned hist[4][kBins];                      // by lane % 4
+  unsigned bins[2][kBins];                      // the CTA's sums, by pass parity
+  unsigned coarse[2][kSelWarps];                // and those of 64 bins
   int warp_above[kSelWarps], warp_eq[kSelWarps];
   int above, eq;                                // the CTA's counts
-  unsigned scan[kSelWarps];
   unsigned digit, left;
   unsigned skip;                                // a timeout is recorded: do nothing
 };
@@ -63,6 +69,16 @@ __device__ __forceinline__ unsigned ld_cluster(uint32_t addr) {
   unsigned v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+
+// Inclusive sum over the lanes from this one up.
+__device__ __forceinline__ unsigned sum_from_lane(unsigned x) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_down_sync(0xffffffffu, x, o);
+    if (lane_id() + o < 32) x += y;
+  }
+  return x;
 }
 
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs A) {
@@ -88,6 +104,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   if (n <= A.budget) {
     for (int i = rank * kSelThreads + tid; i < A.budget; i += cl * kSelThreads)
       idx[i] = i < n ? i : -1;
+    cluster_sync();                             // the others may still read sm.skip
     return;
   }
   const float* mass = A.mass + b * A.ld;
@@ -96,7 +113,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   // each warp of the cluster has a run of `seg` slots, each CTA 32 such runs
   const int warps = cl * kSelWarps;
   const int seg = ((n + warps - 1) / warps + 31) / 32 * 32;
-  const int base = rank * kSelWarps * seg, end = min(n, base + kSelWarps * seg);
+  const int base = min(n, rank * kSelWarps * seg), end = min(n, base + kSelWarps * seg);
+  const int s0 = min(n, base + warp * seg), s1 = min(n, s0 + seg);      // the warp's run
   const bool in_smem = kSelWarps * seg <= kSelKeys;
   auto key = [&](int i) { return in_smem ? kept_keys[i - base] : total_key(__ldg(mass + i)); };
   if (in_smem) {
@@ -109,79 +127,91 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   unsigned thr = 0xffffffffu;
   int ties = 0;
   if (want > 0) {
+    for (int i = tid; i < 4 * kBins; i += kSelThreads) (&sm.hist[0][0])[i] = 0;
+    __syncthreads();
     unsigned prefix = 0, left = static_cast<unsigned>(want);
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < 4 * 2048; i += kSelThreads) (&sm.hist[0][0])[i] = 0;
-      __syncthreads();
-      const int i1 = min(end, hi);
-#pragma unroll 4
-      for (int i = max(base, lo) + tid; i < i1; i += kSelThreads) {
-        const unsigned k = key(i);
-        if (pass == 0 || (k >> (shift + bits)) == prefix)
-          atomicAdd(&sm.hist[lane & 3][(k >> shift) & ((1u << bits) - 1)], 1u);
+      const unsigned mask = (1u << bits) - 1;
+      unsigned* hist = sm.hist[lane & 3];
+#pragma unroll 1
+      for (int i = max(s0, lo) + lane; i < min(s1, hi); i += 32) {
+        const unsigned x = key(i);
+        if (pass == 0 || (x >> (shift + bits)) == prefix)
+          atomicAdd(hist + ((x >> shift) & mask), 1u);
       }
       __syncthreads();
-      for (int d = tid; d < 2048; d += kSelThreads)
-        sm.hist[0][d] += sm.hist[1][d] + sm.hist[2][d] + sm.hist[3][d];
-      cluster_sync();
-      // this thread's two digits, from the top: 2047 - 2 tid and the one below
-      unsigned c0 = 0, c1 = 0;
+      // this thread's two bins: added up, and empty again for the next pass
+      unsigned two[2];
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        if (r >= cl) continue;
-        const uint32_t at = mapa(smem_u32(&sm.hist[0][2046 - 2 * tid]), r);
-        uint32_t lo2, hi2;
-        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
-                     : "=r"(lo2), "=r"(hi2)
-                     : "r"(at)
-                     : "memory");
-        c1 += lo2;
-        c0 += hi2;
-      }
-      unsigned x = c0 + c1;
+      for (int e = 0; e < 2; ++e) {
+        two[e] = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        for (int c = 0; c < 4; ++c) {
+          two[e] += sm.hist[c][2 * tid + e];
+          sm.hist[c][2 * tid + e] = 0;
+        }
+        sm.bins[pass & 1][2 * tid + e] = two[e];
       }
-      if (lane == 31) sm.scan[warp] = x;
+      const unsigned all = __reduce_add_sync(0xffffffffu, two[0] + two[1]);
+      if (lane == 0) sm.coarse[pass & 1][warp] = all;
+      cluster_sync();                           // (every CTA has read the pass before's, too)
+      if (warp == 0) {
+        // the 64 bins that hold the left-th largest, then the bin
+        unsigned x = 0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+          if (r < cl) x += ld_cluster(mapa(smem_u32(&sm.coarse[pass & 1][lane]), r));
+        unsigned from = sum_from_lane(x);
+        const int group = 31 - __clz(__ballot_sync(0xffffffffu, from >= left));
+        unsigned rest = left - __shfl_sync(0xffffffffu, from - x, group);
+        unsigned c0 = 0, c1 = 0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          if (r >= cl) continue;
+          const uint32_t at = mapa(smem_u32(&sm.bins[pass & 1][64 * group + 2 * lane]), r);
+          uint32_t v0, v1;
+          asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];"
+                       : "=r"(v0), "=r"(v1)
+                       : "r"(at)
+                       : "memory");
+          c0 += v0;
+          c1 += v1;
+        }
+        from = sum_from_lane(c0 + c1);
+        const int pair = 31 - __clz(__ballot_sync(0xffffffffu, from >= rest));
+        rest -= __shfl_sync(0xffffffffu, from - c0 - c1, pair);
+        if (lane == pair) {
+          const bool upper = rest <= c1;
+          sm.digit = static_cast<unsigned>(64 * group + 2 * pair + (upper ? 1 : 0));
+          sm.left = rest - (upper ? 0 : c1);
+        }
+      }
       __syncthreads();
-      unsigned above = x - (c0 + c1);
-      for (int w = 0; w < warp; ++w) above += sm.scan[w];
-      if (above < left && left <= above + c0 + c1) {
-        const bool upper = left <= above + c0;
-        sm.digit = static_cast<unsigned>(2047 - 2 * tid - (upper ? 0 : 1));
-        sm.left = left - above - (upper ? 0 : c0);
-      }
-      cluster_sync();                           // also: no CTA reads another's histogram any more
       prefix = (prefix << bits) | sm.digit;
       left = sm.left;
     }
     thr = prefix;
     ties = static_cast<int>(left);
-  } else {
-    __syncthreads();
   }
   // counts of the warp's run, then of everything before it
-  const int s0 = min(n, base + warp * seg), s1 = min(n, s0 + seg);
   auto classify = [&](int i, unsigned& above, unsigned& eq) {
     bool a = false, e = false;
     if (i < s1) {
       if (i < lo || i >= hi) {
         a = true;
       } else if (want > 0) {
-        const unsigned k = key(i);
-        a = k > thr;
-        e = k == thr;
+        const unsigned x = key(i);
+        a = x > thr;
+        e = x == thr;
       }
     }
     above = __ballot_sync(0xffffffffu, a);
     eq = __ballot_sync(0xffffffffu, e);
   };
   int n_above = 0, n_eq = 0;
-#pragma unroll 4
+#pragma unroll 1
   for (int i = s0; i < s1; i += 32) {
     unsigned a, e;
     classify(i + lane, a, e);
@@ -193,32 +223,29 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
     sm.warp_eq[warp] = n_eq;
   }
   __syncthreads();
-  if (tid == 0) {
-    int a = 0, e = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      a += sm.warp_above[w];
-      e += sm.warp_eq[w];
+  const int w_above = sm.warp_above[lane], w_eq = sm.warp_eq[lane];     // (32 warps)
+  int above_before = __reduce_add_sync(0xffffffffu, lane < warp ? w_above : 0);
+  int eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? w_eq : 0);
+  if (warp == 0) {
+    const int a = __reduce_add_sync(0xffffffffu, w_above), e = __reduce_add_sync(0xffffffffu, w_eq);
+    if (lane == 0) {
+      sm.above = a;
+      sm.eq = e;
     }
-    sm.above = a;
-    sm.eq = e;
   }
   cluster_sync();
-  int above_before = 0, eq_before = 0;
   for (int r = 0; r < rank; ++r) {
     above_before += static_cast<int>(ld_cluster(mapa(smem_u32(&sm.above), r)));
     eq_before += static_cast<int>(ld_cluster(mapa(smem_u32(&sm.eq), r)));
   }
-  for (int w = 0; w < warp; ++w) {
-    above_before += sm.warp_above[w];
-    eq_before += sm.warp_eq[w];
-  }
   const unsigned below = (1u << lane) - 1;
-#pragma unroll 2
+#pragma unroll 1
   for (int i = s0; i < s1; i += 32) {
     unsigned a, e;
     classify(i + lane, a, e);
     const int ra = above_before + __popc(a & below), re = eq_before + __popc(e & below);
-    if (((a >> lane) & 1u) || (((e >> lane) & 1u) && re < ties)) idx[ra + min(ties, re)] = i + lane;
+    if (((a >> lane) & 1u) || (((e >> lane) & 1u) && re < ties))
+      idx[ra + min(ties, re)] = i + lane;
     above_before += __popc(a);
     eq_before += __popc(e);
   }
