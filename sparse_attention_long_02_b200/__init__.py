@@ -475,6 +475,16 @@ def _rank(t, n):
     return t.shape
 
 
+_I32_MAX = 2**31 - 1
+
+
+def _count(v, name):
+    """A count the C interface takes as int32, refused where it would wrap."""
+    if not -_I32_MAX <= v <= _I32_MAX:
+        raise ValueError(f"{name} = {v} does not fit 32 bits")
+    return v
+
+
 def _new(stream, make, *args, **kw):
     """A tensor made by torch in the memory of the stream that will use it."""
     if stream is None:
@@ -547,10 +557,12 @@ def window_mla_decode_paged(q, kv_pool, block_table, seq_len, sinks, window, sm_
     """Attention of the new tokens over a sliding window of the paged latent cache
     and its first `sinks` tokens -> (out, lse); workspace as split_mla_decode_paged."""
     return _range_decode("dsa_window_mla_decode_paged", q, kv_pool, block_table, seq_len,
-                         (sinks, window), sm_scale, out, lse, workspace, stream)
+                         (_count(sinks, "sinks"), _count(window, "window")), sm_scale, out, lse, workspace, stream)
 
 
 def window_mla_workspace_size(T, S, H, q_pos0, sinks, window) -> int:
+    for v, name in ((q_pos0, "q_pos0"), (sinks, "sinks"), (window, "window")):
+        _count(v, name)
     return int(_lib.dsa_window_mla_workspace_size(T, S, H, q_pos0, sinks, window))
 
 
@@ -563,6 +575,8 @@ def window_mla(q, kv, sinks, window, sm_scale, q_pos0=0, out=None, lse=None, wor
     S = _rank(kv, 2)[0]
     _fit(q, dev, torch.bfloat16, T, H, 576)
     _fit(kv, dev, torch.bfloat16, S, 576)
+    for v, name in ((q_pos0, "q_pos0"), (sinks, "sinks"), (window, "window")):
+        _count(v, name)
     out, lse = _outputs(dev, stream, out, lse, T, H)
     ws = _scratch(workspace, lambda: window_mla_workspace_size(T, S, H, q_pos0, sinks, window), dev,
                   stream)
@@ -601,6 +615,8 @@ def cache_evict_paged(kv_pool, block_table, seq_len, mass, budget, sinks, recent
         _fit(k8_pool, dev, torch.uint8, nblk, 64, 128)
     if k_scale_pool is not None:
         _fit(k_scale_pool, dev, torch.float32, nblk, 64)
+    for v, name in ((budget, "budget"), (sinks, "sinks"), (recent, "recent")):
+        _count(v, name)
     keep = max(budget, 0)
     if idx is None:
         idx = _new(stream, torch.empty, B, keep, dtype=torch.int32, device=dev)

@@ -704,6 +704,25 @@ def test_workspace_ends_where_it_says(dsa):
     no_device_error(dsa)
 
 
+def test_counts_past_32_bits_are_refused(dsa):
+    q = torch.zeros(2, 4, 576, dtype=torch.bfloat16, device="cuda")
+    pool = torch.zeros(2, 64, 576, dtype=torch.bfloat16, device="cuda")
+    bt = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    sl = torch.ones(1, dtype=torch.int32, device="cuda")
+    mass = torch.zeros(1, 64, device="cuda")
+    big = 2**32 + 1
+    for call in (lambda: dsa.window_mla(q, pool[0], 1, big, SM),
+                 lambda: dsa.window_mla(q, pool[0], big, 8, SM),
+                 lambda: dsa.window_mla(q, pool[0], 1, 8, SM, q_pos0=big),
+                 lambda: dsa.window_mla_decode_paged(q[:1, None], pool, bt, sl, 1, big, SM),
+                 lambda: dsa.window_mla_decode_paged(q[:1, None], pool, bt, sl, big, 1, SM),
+                 lambda: dsa.cache_evict_paged(pool, bt, sl, mass, big, 0, 0),
+                 lambda: dsa.cache_evict_paged(pool, bt, sl, mass, 8, big, 0),
+                 lambda: dsa.cache_evict_paged(pool, bt, sl, mass, 8, 0, big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+
+
 def test_outputs_on_any_16_byte_boundary(dsa):
     """Outputs and inputs that start 16 bytes into an allocation."""
     g = torch.Generator(device="cuda").manual_seed(95)

@@ -121,3 +121,15 @@ def test_binding_refuses_tensors_that_do_not_fit(dsa):  # noqa: F811
         dsa.window_mla(q[0], kv[0], 0, 4, 0.1)
     with pytest.raises(ValueError):
         dsa.cache_evict_paged(kv, bt, sl, torch.zeros(1, 128), 10, 0, 0)
+
+
+@pytest.mark.parametrize("arg", [3, 4, 5])
+@pytest.mark.parametrize("value", [2**31, 2**32 + 1, -2**32])
+def test_counts_past_32_bits_are_refused(arg, value):
+    from sparse_attention_long_02_b200 import window_mla_workspace_size
+
+    args = [4, 100, 128, 0, 1, 64]
+    window_mla_workspace_size(*args)
+    args[arg] = value
+    with pytest.raises(ValueError, match="32 bits"):
+        window_mla_workspace_size(*args)
