@@ -19,13 +19,15 @@
 // give the kept slots in order without a scan per step.
 //
 // evict_move_kernel: a row's destination is never behind its source slot, so a
-// CTA that walks the kept rows in order, reading a step's rows before it writes
-// them, never overwrites a row it has still to read (nor one of the next step,
-// which it reads ahead). The bytes of a row are split by column, each slice of
-// columns moved by CTAs of its own: none reads what another slice's write. A
-// slice's rows are split over a cluster of CTAs where there are few sequences;
-// the cluster's barrier then stands between a step's reads and its writes.
-// Bound by HBM, each moved byte read and written once.
+// walk over the kept rows in order that reads a step's rows before it writes them
+// never overwrites a row it has still to read, nor one of later steps, which it
+// may read ahead. A cluster of up to 8 CTAs walks a sequence, its rows split over
+// them, with the cluster's barrier between a step's reads and its writes. Where
+// there are few sequences the bytes of a row are split by column too, each slice
+// moved by a cluster of its own: none reads what another slice's write. Bound by
+// HBM, each moved byte read and written once (64 x 32768 -> 16384 tokens: 481 us
+// with the selection, 5.6 TB/s), and for few sequences by the latency of a step's
+// chain (read, barrier, write).
 #include "common.cuh"
 #include "dsa_internal.h"
 
@@ -36,12 +38,11 @@ constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelKeys = 40960;                 // keys a CTA keeps in shared memory
 constexpr int kBins = 2048;
-// CTAs of 512 threads and four rows a thread and step where few sequences leave
-// latency to hide; of 256 and two, more of them on an SM and a shorter last
-// wave, for many (64 x 32768 -> 16384: 557 us; 627 us with the former).
-constexpr int kFewThreads = 512, kFewRows = 4;
-constexpr int kManyThreads = 256, kManyRows = 2;
-constexpr int kMoveWant = 2 * 148;              // CTAs a move should have, in clusters of up to 8
+// Two CTAs of 1024 threads fit an SM. (64 x 32768 -> 16384 took 519 us with 512
+// threads, two rows a thread and four steps, 556 us with 1024, two and three.)
+constexpr int kMoveThreads = 1024;
+constexpr int kDepth = 3;                       // steps of a move in shared memory
+constexpr int kMoveWant = 256, kMoveMost = 296; // CTAs that move latent rows, at least and at most
 
 // Order-preserving key of a total; NaN below everything, -0 equal to +0.
 __device__ __forceinline__ unsigned total_key(float v) {
@@ -252,92 +253,114 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   cluster_sync();                               // the others may still read this CTA's counts
 }
 
-// One column slice of one sequence: `cols` elements from element `first` of
-// every row (rows of `pitch` elements), kMoveRows * threads / cols rows a CTA
-// and step. The next step's rows are on their way while a step's are written.
-template <int kMoveThreads, int kMoveRows, typename V>
-__device__ __forceinline__ void move_columns(const EvictArgs& A, int b, int count, const V* from,
-                                             V* to, bool paged, int pitch, int cols, int first) {
-  const int cl = static_cast<int>(cluster_size());
-  const int per = kMoveThreads / cols * cl;     // the cluster's rows of one sub-step
-  const int col = first + static_cast<int>(threadIdx.x) % cols;
-  const int sub = kMoveThreads / cols * static_cast<int>(cluster_rank()) +
-                  static_cast<int>(threadIdx.x) / cols;
-  const int* idx = A.idx + static_cast<long long>(b) * A.budget;
-  const int* table = A.block_table + static_cast<long long>(b) * A.max_blocks;
-  auto row = [&](int s) -> long long {
-    if (!paged) return s;
-    const int pb = __ldg(table + (s >> 6));
-    return pb < 0 || pb >= A.nblk ? -1 : static_cast<long long>(pb) * 64 + (s & 63);
-  };
-  V v[2][kMoveRows];
-  int src[kMoveRows];
-  auto slots = [&](int j0) {
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int j = j0 + u * per + sub;
-      src[u] = j < count ? __ldg(idx + j) : -1;
-    }
-  };
-  auto load = [&](int j0, V (&w)[kMoveRows]) {
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int j = j0 + u * per + sub;
-      if (src[u] < 0 || (src[u] == j && from == to)) continue;
-      const long long r = row(src[u]);
-      if (r >= 0) w[u] = from[r * pitch + col];
-    }
-  };
-  const int step = kMoveRows * per;
-  slots(0);
-  load(0, v[0]);
-  int ph = 0;
-  for (int j0 = 0; j0 < count; j0 += step, ph ^= 1) {
-    int at[kMoveRows];
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) at[u] = src[u];
-    slots(j0 + step);
-    if (ph == 0)
-      load(j0 + step, v[1]);
-    else
-      load(j0 + step, v[0]);
-    // the step's rows are read
-    if (cl > 1)
-      cluster_sync();
-    else
-      __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int j = j0 + u * per + sub;
-      if (at[u] < 0 || (at[u] == j && from == to)) continue;
-      const long long r = row(j);
-      if (r < 0 || row(at[u]) < 0)
-        raise_error(A.err, kErrBounds);
-      else
-        to[r * pitch + col] = ph == 0 ? v[0][u] : v[1][u];
-    }
-  }
+struct MoveSmem {                               // places by step and thread
+  uint4 row[kDepth][kMoveThreads];
+  int dst[kDepth][kMoveThreads];                // the row it goes to, -1: nowhere
+};
+template <int kBytes>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (kBytes == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(kBytes)
+                 : "memory");
 }
 
-// kCols: 16-byte columns of a slice (divides 8 and 72).
-template <int kCols, int kMoveThreads, int kMoveRows>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs A) {
-  const int b = static_cast<int>(blockIdx.y);
+// One column slice of one sequence: `cols` elements from element `first` of
+// every row (rows of `pitch` elements), threads / cols rows a CTA and step.
+// Rows pass through shared memory, each thread's in places of its own, with
+// kDepth - 1 steps' reads on their way; a step's table entries are loaded a step
+// before its reads, and its slots a step before that.
+//
+// Between a step's reads and its writes stands a barrier that orders nothing
+// else: no thread reads what another has written, and a read is over once it
+// has landed. So the arrival is relaxed (one that releases waits for all reads
+// and writes in flight, the next steps' too: 8 x 32768 -> 16384 took 161 us).
+template <typename V>
+__device__ __forceinline__ void move_columns(const EvictArgs& A, MoveSmem& sm, int b, int count,
+                                             const V* from, V* to, bool paged, int pitch, int cols,
+                                             int first) {
+  const int cl = static_cast<int>(cluster_size()), tid = static_cast<int>(threadIdx.x);
+  const int rows = kMoveThreads / cols, col = first + tid % cols;
+  const int step = rows * cl, sub = rows * static_cast<int>(cluster_rank()) + tid / cols;
+  const int end = tid < rows * cols ? count : 0;                // (threads past the last row are idle)
+  const int* idx = A.idx + static_cast<long long>(b) * A.budget;
+  const int* table = A.block_table + static_cast<long long>(b) * A.max_blocks;
+  int src, slot, src_block, dst_block;
+  auto slots = [&](int j) { src = j < end ? __ldg(idx + j) : -1; };
+  auto blocks = [&](int j) {
+    const bool moves = src >= 0 && !(src == j && from == to);
+    slot = moves ? src : -1;
+    src_block = moves && paged ? __ldg(table + (src >> 6)) : 0;
+    dst_block = moves && paged ? __ldg(table + (j >> 6)) : 0;
+  };
+  auto read = [&](int j, int d) {
+    int dst = -1;
+    if (slot >= 0) {
+      if (paged && (src_block < 0 || src_block >= A.nblk || dst_block < 0 || dst_block >= A.nblk)) {
+        raise_error(A.err, kErrBounds);
+      } else {
+        const int r = paged ? src_block * 64 + (slot & 63) : slot;
+        dst = paged ? dst_block * 64 + (j & 63) : j;
+        copy_async<sizeof(V)>(smem_u32(&sm.row[d][tid]),
+                              from + static_cast<long long>(r) * pitch + col);
+      }
+    }
+    sm.dst[d][tid] = dst;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  int next = sub;                               // this thread's row of the step read next
+  slots(next);
+  blocks(next);
+  slots(next + step);
+#pragma unroll 1
+  for (int d = 0; d + 1 < kDepth; ++d, next += step) {
+    read(next, d);
+    blocks(next + step);
+    slots(next + 2 * step);
+  }
+  int d = 0;
+#pragma unroll 1
+  for (int j0 = 0; j0 < count; j0 += step, next += step) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+    if (cl > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    read(next, d == 0 ? kDepth - 1 : d - 1);
+    blocks(next + step);
+    slots(next + 2 * step);
+    if (cl > 1)
+      cluster_wait();
+    else
+      __syncthreads();
+    const int dst = sm.dst[d][tid];
+    if (dst >= 0)
+      to[static_cast<long long>(dst) * pitch + col] = *reinterpret_cast<V*>(&sm.row[d][tid]);
+    d = d + 1 == kDepth ? 0 : d + 1;
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// Job y of a sequence: a slice of the latent rows' 72 16-byte columns, then the
+// indexer's keys, their scales and the totals.
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs A, int slices) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  MoveSmem& sm = *reinterpret_cast<MoveSmem*>(smem_raw);
+  const int b = static_cast<int>(blockIdx.x / cluster_size());
   if (__syncthreads_or(launch_aborted(A.err))) return;
   const int count = A.seq_len_out[b];
-  constexpr int kKv = 72 / kCols, kK8 = 8 / kCols;
-  int s = static_cast<int>(blockIdx.x / cluster_size());
-  if (s < kKv) {
+  const int job = static_cast<int>(blockIdx.y);
+  if (job < slices) {
     uint4* p = static_cast<uint4*>(A.kv_pool);
-    move_columns<kMoveThreads, kMoveRows, uint4>(A, b, count, p, p, true, 72, kCols, kCols * s);
-  } else if ((s -= kKv) < kK8) {
+    const int cols = 72 / slices;
+    move_columns<uint4>(A, sm, b, count, p, p, true, 72, cols, cols * job);
+  } else if (job == slices) {
     uint4* p = static_cast<uint4*>(A.k8_pool);
-    if (p) move_columns<kMoveThreads, kMoveRows, uint4>(A, b, count, p, p, true, 8, kCols, kCols * s);
-  } else if (s == kK8) {
+    if (p) move_columns<uint4>(A, sm, b, count, p, p, true, 8, 8, 0);
+  } else if (job == slices + 1) {
     if (A.k_scale_pool)
-      move_columns<kMoveThreads, kMoveRows, float>(A, b, count, A.k_scale_pool, A.k_scale_pool, true, 1, 1, 0);
+      move_columns<float>(A, sm, b, count, A.k_scale_pool, A.k_scale_pool, true, 1, 1, 0);
   } else if (A.mass_out) {
-    move_columns<kMoveThreads, kMoveRows, float>(A, b, count, A.mass + b * A.ld, A.mass_out + b * A.ld_out, false, 1, 1, 0);
+    move_columns<float>(A, sm, b, count, A.mass + b * A.ld, A.mass_out + b * A.ld_out, false, 1,
+                        1, 0);
   }
 }
 
@@ -365,23 +388,22 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st) {
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
   if (e != cudaSuccess) return e;
-  // 128-byte slices (whole lines), in clusters as large as leave two CTAs an SM
-  // or so; a few sequences get 64-byte slices too
-  constexpr int kWide = 9 + 1 + 2, kNarrow = 18 + 2 + 2;
-  const bool many = a.B * kWide >= 2 * kMoveWant;
-  const bool narrow = a.B * kWide * 8 < kMoveWant;
-  const int slices = narrow ? kNarrow : kWide;
+  // Whole rows where the sequences' clusters fill the GPU, else as few slices of
+  // them as do, of 384, 128 or 64 bytes (measured with 512 threads a CTA, 64 x
+  // 32768 -> 16384: 515 us in whole rows, 613 us in three slices and 626 us in
+  // nine; 16 x 32768: 214 us in whole rows, 194 us in three slices)
+  int slices = 1;
+  while (slices < 18 && a.B * slices * 8 < kMoveWant) slices = slices == 9 ? 18 : 3 * slices;
   cl = 1;
-  while (cl < 8 && a.B * slices * cl * 2 <= kMoveWant) cl *= 2;
-  cfg.gridDim = dim3(static_cast<unsigned>(slices * cl), static_cast<unsigned>(a.B));
-  cfg.blockDim = dim3(many ? kManyThreads : kFewThreads);
-  cfg.dynamicSmemBytes = 0;
+  while (cl < 8 && a.B * slices * cl * 2 <= kMoveMost) cl *= 2;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.B * cl), static_cast<unsigned>(slices + 3));
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = sizeof(MoveSmem);
   at.val.clusterDim.x = static_cast<unsigned>(cl);
-  return cudaLaunchKernelEx(&cfg,
-                            many     ? evict_move_kernel<8, kManyThreads, kManyRows>
-                            : narrow ? evict_move_kernel<4, kFewThreads, kFewRows>
-                                     : evict_move_kernel<8, kFewThreads, kFewRows>,
-                            a);
+  e = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(cfg.dynamicSmemBytes));
+  if (e != cudaSuccess) return e;
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, slices);
 }
 
 }  // namespace dsa
