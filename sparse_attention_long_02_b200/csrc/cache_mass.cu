@@ -35,7 +35,6 @@ constexpr int kUnit = 64 * 128;
 // Even, so that each of the two loading warps has its own places.
 constexpr int kRing = 4;
 constexpr int kCtas = 148;                      // one an SM
-constexpr int kMinShare = 1;
 
 struct MassSmem {
   uint8_t q[9][kChunk];
@@ -90,7 +89,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   unsigned* err = A.err;
   const int warp = warp_id(), lane = lane_id();
   find_share<kThreads>(sm.share, sm.sums, A.B, static_cast<int>(blockIdx.x),
-                       static_cast<int>(gridDim.x), kMinShare, 0, [&](int b) {
+                       static_cast<int>(gridDim.x), 0, [&](int b) {
                          const int len = A.seq_len[b];
                          if (blockIdx.x == 0 && (len < 0 || len > A.max_blocks * 64))
                            raise_error(err, kErrBounds);

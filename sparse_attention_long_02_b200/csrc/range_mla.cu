@@ -34,11 +34,25 @@
 //
 // Work split. The tiles of all row tiles form one list; each cluster takes an
 // equal share of it, wherever it begins and ends (or whole row tiles in turn,
-// where that is as fast as equal shares and the join they need). A row tile inside one share
-// is written directly; one cut over several clusters leaves its parts (fp32
-// sums of p v with the row's maximum and sum) in the workspace, which
+// where that is as fast as equal shares and the join they need). A row tile
+// inside one share is written directly; one cut over several clusters leaves its
+// parts (fp32 sums of p v with the row's maximum and sum) in the workspace, which
 // range_join_kernel combines: with m = max m_i, l = sum l_i 2^(m_i - m),
 // O = sum O_i 2^(m_i - m) / l.
+//
+// What bounds it. A tile's MMAs take CTA 0 2400 cycles and CTA 1 2050, and CTA
+// 0's shared memory takes 368 KB a tile in and out (K in and to the MMA, the rope
+// dims of Q, P in and out), 2900 cycles at 128 B each. Measured, a tile takes 3740
+// cycles with the cache in L2 (64 sequences of 32768 tokens that share 37 MB: 503
+// us) and 4440 from HBM (620 to 650 us, 3.8 TB/s), where QK waits for K in 1900 of
+// them. That run is held at 1.5 GHz of 1.97 by the board's 1000 W; short calls run
+// at full clock, and their time is the way to the first tile (9 us), the shares'
+// tiles (2.4 us each), a part's way to memory (5 us: an SM writes some 30 B a
+// cycle) and the join (7 us): one sequence of 131072 tokens 66 us. A deeper ring for K
+// does not pay: its memory has to come from the stagings of P, and the softmax
+// then waits for its copies (one staging a unit and five entries: 707 us for 511
+// with the cache in L2; three and a place of its own for K's rope dims: 580 us),
+// and entries of 16 KB cost a wait and a commit more each (598 us).
 #include <algorithm>
 
 #include "common.cuh"
@@ -65,9 +79,11 @@ constexpr float kRebase = 8.0f;                 // lazy rescale threshold (log2 
 constexpr int kMaxClusters = 74;                // two CTAs on each of 148 SMs
 constexpr int kScanItems = 16384;               // row tiles a cluster scans for its share
 constexpr int kItemCost = 3;                    // a row tile's fixed cost, in tiles
-constexpr int kMinShare = 2;                    // tiles (and fixed costs) a cluster takes at least
 // What cutting row tiles costs, in tiles: where there are fewer of them than
-// clusters a cluster writes one part, else two.
+// clusters a cluster writes one part, else two. (Two queries of 64 sequences in a
+// window of 2048: 106 us whole, 118 us cut; a prompt of 8191 rows and a window of
+// 1024: 2.77 ms whole, 2.84 ms cut; 64 x 32768 tokens: 683 us whole, 656 us cut;
+// one sequence of 131072: 2393 us whole, 67 us cut.)
 constexpr int kCutCostFew = 5, kCutCostMany = 7;
 
 struct LogitsSmem {                             // CTA 0
@@ -352,8 +368,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
   } else {
     find_share<kThreads>(ctl.share, reinterpret_cast<long long*>(big), A.items, cluster,
-                         A.clusters, kMinShare,
-                         A.items < A.clusters ? kCutCostFew : kCutCostMany, [&](int i) {
+                         A.clusters, A.items < A.clusters ? kCutCostFew : kCutCostMany,
+                         [&](int i) {
                            if (A.block_table && blockIdx.x == 0) {
                              const int len = A.seq_len[i / A.per_seq];
                              if (len < 0 || len > A.max_blocks * 64) raise_error(err, kErrBounds);
@@ -399,8 +415,9 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp == 0 || warp == 2) {
       // ------------------------------------------------ Q and K loads (CTA 0)
       // Two warps take the ring's entries in turn: a wait, an expect and four
-      // loads cost one thread about 540 cycles, an entry's MMAs 549. In a
-      // piece's first tile each K entry follows the Q entry it meets.
+      // loads cost one thread about 540 cycles (1200 while the TMA unit is busy
+      // with others), an entry's MMAs 549. In a piece's first tile each K entry
+      // follows the Q entry it meets.
       const int par = warp >> 1;
       if (lane == 0) {
         int ent = 0, ropes = 0;
@@ -1010,10 +1027,16 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // tile, 16 dims a warp; where the row tile has many parts, 8 dims, whose parts
 // the eight warps share. The weights are worked out once a task. A warp reads
 // 512 consecutive bytes at a time (four dims of 32 rows), eight reads in
-// flight, the first of them asked for before the weights are known.
+// flight, the first of them asked for before the weights are known. Bound by
+// the latency of a task's chain (record, maxima, weights, sums), so tasks are
+// few and large: one sequence of 131072 tokens, 73 parts of 256 KB, 7 us with the
+// launch (13 us in tasks of 32 dims with the weights worked out for each); 33
+// sequences of up to 32768, two queries each, 9 us (20 us).
 constexpr int kJoinThreads = 256, kJoinResident = 3, kJoinCtas = kJoinResident * 148;
 constexpr int kJoinBatch = (kMaxClusters + 7) / 8;              // parts a warp weighs
 constexpr int kJoinRecs = (kMaxClusters + 31) / 32;             // records a lane looks at
+// Parts from which the warps share them (33 ragged sequences, two queries each:
+// 95 us with 16, 97 us with 8; one of 131072 tokens has 73 and is the same).
 constexpr int kJoinMany = 16;
 constexpr int kJoinFewDims = 4, kJoinManyDims = 2;              // a warp's dims, in fours
 struct JoinSmem {
@@ -1188,7 +1211,7 @@ size_t range_layout(RangeArgs& a, void* workspace) {
   const long long tiles = (units + 1) / 2;
   a.whole = !a.block_table && items > kScanItems;
   a.clusters = static_cast<int>(std::min<long long>(
-      kMaxClusters, std::max(1ll, items * (tiles + kItemCost) / kMinShare)));
+      kMaxClusters, std::max(1ll, items * (tiles + kItemCost))));
   a.rows_pad = (a.G * a.H + 7) / 8 * 8;
   if (a.whole || a.clusters == 1) {
     a.rec = nullptr;

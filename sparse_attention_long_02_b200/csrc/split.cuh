@@ -65,7 +65,7 @@ __device__ __forceinline__ long long share_begin(long long total, int parts, int
   return total * c / parts;
 }
 
-// Finds share `c` of at most `parts_max`, each of `min_share` weight at least.
+// Finds share `c` of at most `parts_max`, each of one unit of weight at least.
 // Where items taken whole, in turn, are as fast as equal shares and `cut_cost`
 // (weight that a cut costs; 0: always cut), the share says so instead. Called
 // by all kThreads threads; `sums` is scratch for two numbers a warp; weight(i)
@@ -73,8 +73,7 @@ __device__ __forceinline__ long long share_begin(long long total, int parts, int
 // Shares past the last part get item = items.
 template <int kThreads, typename Weight>
 __device__ __forceinline__ void find_share(Share& sh, long long* sums, int items, int c,
-                                           int parts_max, int min_share, int cut_cost,
-                                           Weight weight) {
+                                           int parts_max, int cut_cost, Weight weight) {
   const int tid = static_cast<int>(threadIdx.x);
   const int per = (items + kThreads - 1) / kThreads;
   const int i0 = min(items, tid * per), i1 = min(items, i0 + per);
@@ -112,7 +111,7 @@ __device__ __forceinline__ void find_share(Share& sh, long long* sums, int items
     w_max = max(w_max, static_cast<int>(sums[kThreads / 32 + w]));
   }
   const int parts = static_cast<int>(
-      max(1ll, min(static_cast<long long>(parts_max), total / min_share)));
+      max(1ll, min(static_cast<long long>(parts_max), total)));
   if (tid == 0) {
     sh.total = total;
     sh.parts = parts;
