@@ -111,7 +111,7 @@ def _check(status, where):
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()          # (the signatures make it a pointer)
 
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -119,9 +119,9 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 def _stream(stream=None):
     if stream is None and _raw_stream is not None:      # the same handle, without a Stream object
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+        return _raw_stream(torch.cuda.current_device())
     s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    return s.cuda_stream
 
 
 def _u8(t):

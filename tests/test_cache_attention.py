@@ -548,6 +548,13 @@ def test_evict_long(dsa):
     check_evict(dsa, [3000] * 150, 700, 4, 100, tied, seed=46)
 
 
+@pytest.mark.parametrize("B", [2, 5, 12, 31, 33, 75, 160])
+def test_evict_batches(dsa, B):
+    """Each way rows are split: column slices, clusters of eight to one."""
+    lens = [(37 + 211 * b) % 1900 for b in range(B)]
+    check_evict(dsa, lens, 417, 5, 61, tied if B % 2 else heavy, seed=48 + B, alias=B > 30)
+
+
 def test_evict_bad_pages_and_lengths(dsa):
     c = make_cache([500, 500], 47, poison=False)
     mass = torch.rand(2, 512, generator=c["g"], device="cuda")
