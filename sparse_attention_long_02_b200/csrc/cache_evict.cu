@@ -286,6 +286,8 @@ __device__ __forceinline__ void move_columns(const EvictArgs& A, MoveSmem& sm, i
   const int end = tid < rows * cols ? count : 0;                // (threads past the last row are idle)
   const int* idx = A.idx + static_cast<long long>(b) * A.budget;
   const int* table = A.block_table + static_cast<long long>(b) * A.max_blocks;
+  // (the last kept row in its place: so are all before it)
+  if (from == to && (count == 0 || __ldg(idx + count - 1) == count - 1)) return;
   int src, slot, src_block, dst_block;
   auto slots = [&](int j) { src = j < end ? __ldg(idx + j) : -1; };
   auto blocks = [&](int j) {
