@@ -42,17 +42,21 @@
 //
 // What bounds it. A tile's MMAs take CTA 0 2400 cycles and CTA 1 2050, and CTA
 // 0's shared memory takes 368 KB a tile in and out (K in and to the MMA, the rope
-// dims of Q, P in and out), 2900 cycles at 128 B each. Measured, a tile takes 3740
-// cycles with the cache in L2 (64 sequences of 32768 tokens that share 37 MB: 503
-// us) and 4440 from HBM (620 to 650 us, 3.8 TB/s), where QK waits for K in 1900 of
-// them. That run is held at 1.5 GHz of 1.97 by the board's 1000 W; short calls run
-// at full clock, and their time is the way to the first tile (9 us), the shares'
-// tiles (2.4 us each), a part's way to memory (5 us: an SM writes some 30 B a
-// cycle) and the join (7 us): one sequence of 131072 tokens 66 us. A deeper ring for K
-// does not pay: its memory has to come from the stagings of P, and the softmax
-// then waits for its copies (one staging a unit and five entries: 707 us for 511
-// with the cache in L2; three and a place of its own for K's rope dims: 580 us),
-// and entries of 16 KB cost a wait and a commit more each (598 us).
+// dims of Q, P in and out), 2900 cycles at 128 B each. Measured, a tile takes some
+// 3500 cycles with the cache in L2 (64 sequences of 32768 tokens that share 37 MB:
+// 472 us) and 4100 from HBM (595 us, 4.1 TB/s), where QK waits for K. That run is
+// held at 1.5 GHz of 1.97 by the board's 1000 W; short calls run at full clock, and
+// their time is the way to the first tile (9 us), the shares' tiles (2 to 2.3 us
+// each), a part's way to memory (5 us: an SM writes some 30 B a cycle) and the join
+// (7 us): one sequence of 131072 tokens 62 us.
+//
+// CTA 0's shared memory is full to the last bytes. The rope dims of K in a place of
+// their own, not in the ring, took 64 x 32768 from 635 to 595 us; what paid for
+// them are the barriers of CTA 1 alone, which live in its own memory, and one
+// buffer of maxima instead of two. Paying with a staging of P instead makes the
+// softmax wait for its copies (three stagings: 580 us with the cache in L2, where
+// it was 508; one a unit and five ring entries: 707), and entries of 16 KB cost a
+// wait and a commit more each (598 us).
 #include <algorithm>
 
 #include "common.cuh"
@@ -87,11 +91,12 @@ constexpr int kItemCost = 3;                    // a row tile's fixed cost, in t
 constexpr int kCutCostFew = 5, kCutCostMany = 7;
 
 struct LogitsSmem {                             // CTA 0
-  uint8_t ring[kRing][kEntry];                  // K, and Q on its way to TMEM
+  uint8_t ring[kRing][kEntry];                  // K's latent dims, and Q on its way to TMEM
+  uint8_t k_rope[kAtom];                        // K dims [512, 576)
   uint8_t p[2][2][kAtom];                       // staging of P, by tile parity and unit
   uint8_t q_rope[kAtom];                        // Q dims [512, 576)
   float alpha[2][128];                          // staging of the rescale factors, by tile parity
-  float mx[2][2][128];                          // maxima, by tile parity and softmax group
+  float mx[2][128];                             // a tile's maxima, by softmax group
 };
 struct OutputSmem {                             // CTA 1
   uint8_t p[kPSlots][kAtom];
@@ -99,6 +104,14 @@ struct OutputSmem {                             // CTA 1
   float alpha[4][128];                          // rescale factors, by tile
   float2 ml[2][128];                            // reference maximum and sum of each softmax group
   uint8_t stage[8][32 * 64];                    // output rows on their way out, by warp
+  unsigned long long v_full[kVRing], v_empty[kVRing];
+  unsigned long long p_full[kPSlots], p_free[kPSlots];
+  unsigned long long al_full[4];                // a tile's rescale factors have landed
+  unsigned long long o_ok[4];                   // O is ready for a tile's PV
+  unsigned long long clean[2];                  // V of a tile's unit with hidden keys is ready
+  unsigned long long pv_done[4];
+  unsigned long long ml_full;
+  unsigned long long piece_done[kPieces];       // the piece's output is on its way
 };
 constexpr size_t kBig = std::max(sizeof(LogitsSmem), sizeof(OutputSmem));
 static_assert(kBig % 1024 == 0, "the control block follows the larger role's memory");
@@ -256,6 +269,7 @@ struct Ctl {
   unsigned long long q_ready[kQPairs];          // 128 dims of Q are in TMEM
   unsigned long long rope_full;
   unsigned long long k_full[kRing], k_empty[kRing];
+  unsigned long long kr_full, kr_empty;         // k_rope
   unsigned long long s_full[2], s_empty[2];     // by tile parity
   unsigned long long mx_bar[4];                 // both groups' maxima of a lane quarter
   // by tile parity and unit, so that whoever waits on one sees every phase
@@ -263,22 +277,13 @@ struct Ctl {
   unsigned long long p_ack[2][2];               // CTA 1 holds the atom: its staging is free
   unsigned long long p_room[kPSlots];           // CTA 1 has room for another atom
   unsigned long long ml_free;                   // CTA 1 has read ml
-  // CTA 1
-  unsigned long long v_full[kVRing], v_empty[kVRing];
-  unsigned long long p_full[kPSlots], p_free[kPSlots];
-  unsigned long long al_full[4];                // a tile's rescale factors have landed
-  unsigned long long o_ok[4];                   // O is ready for a tile's PV
-  unsigned long long clean[2];                  // V of a tile's unit with hidden keys is ready
-  unsigned long long pv_done[4];
   unsigned long long o_done;
-  unsigned long long ml_full;
   Share share;                                  // of the row tiles' weights
   unsigned long long piece_full[kPieces];
-  unsigned long long piece_done[kPieces];       // CTA 1: the piece's output is on its way
   uint32_t tmem_base;
   int abort_flag;
 };
-constexpr size_t kSmemBytes = kBig + sizeof(Ctl) + 1024;
+constexpr size_t kSmemBytes = kBig + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "fits the 227 KB of shared memory a CTA may use");
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -303,8 +308,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                  const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ RangeArgs A) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* big = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                            ~static_cast<uintptr_t>(1023));
+  uint8_t* big = smem_raw;
   LogitsSmem& sl = *reinterpret_cast<LogitsSmem*>(big);
   OutputSmem& so = *reinterpret_cast<OutputSmem*>(big);
   Ctl& ctl = *reinterpret_cast<Ctl*>(big + kBig);
@@ -326,31 +330,33 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       init(ctl.p_own[i >> 1][i & 1], 4);
       init(ctl.p_ack[i >> 1][i & 1], 1);
       init(ctl.p_room[i], 1);
-      init(ctl.v_full[i], 1);
-      init(ctl.v_empty[i], 1);
-      init(ctl.p_full[i], 1);
-      init(ctl.p_free[i], 1);
-      init(ctl.al_full[i], 1);
-      init(ctl.o_ok[i], 8);
-      init(ctl.pv_done[i], 1);
-      // CTA 1 expects the first atoms of P before CTA 0 can send one
       if (rank == 1) {
-        mbar_expect_tx(smem_u32(&ctl.p_full[i]), kAtom);
-        mbar_expect_tx(smem_u32(&ctl.al_full[i]), 512);
+        init(so.v_full[i], 1);
+        init(so.v_empty[i], 1);
+        init(so.p_full[i], 1);
+        init(so.p_free[i], 1);
+        init(so.al_full[i], 1);
+        init(so.o_ok[i], 8);
+        init(so.pv_done[i], 1);
+        // CTA 1 expects the first atoms of P before CTA 0 can send one
+        mbar_expect_tx(smem_u32(&so.p_full[i]), kAtom);
+        mbar_expect_tx(smem_u32(&so.al_full[i]), 512);
       }
     } else if (lane >= 8 && lane < 16) {
       init(ctl.piece_full[i], 1);
-      init(ctl.piece_done[i], 1);
+      if (rank == 1) init(so.piece_done[i], 1);
     } else if (lane == 16 || lane == 17) {
       init(ctl.s_full[i], 1);
       init(ctl.s_empty[i], 8);
-      init(ctl.clean[i], 8);
+      if (rank == 1) init(so.clean[i], 8);
     } else if (lane == 18) {
       init(ctl.q_free, 1);
       init(ctl.rope_full, 1);
+      init(ctl.kr_full, 1);
+      init(ctl.kr_empty, 1);
       init(ctl.ml_free, 8);
       init(ctl.o_done, 1);
-      init(ctl.ml_full, 8);
+      if (rank == 1) init(so.ml_full, 8);
       ctl.abort_flag = launch_aborted(err) ? 1 : 0;
     }
     fence_barrier_init();
@@ -417,10 +423,11 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // Two warps take the ring's entries in turn: a wait, an expect and four
       // loads cost one thread about 540 cycles (1200 while the TMA unit is busy
       // with others), an entry's MMAs 549. In a piece's first tile each K entry
-      // follows the Q entry it meets.
+      // follows the Q entry it meets. The first warp then loads Q's rope dims,
+      // the second those of each tile of K.
       const int par = warp >> 1;
       if (lane == 0) {
-        int ent = 0, ropes = 0;
+        int ent = 0, loaded = 0, ropes = 0;
         for (; next_piece(false); ++pieces) {
           const int q_row = static_cast<int>(x.row0);
           int e0 = unit_entry(A, x, 2 * p.t0), e1 = unit_entry(A, x, 2 * p.t0 + 1);
@@ -430,46 +437,52 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             e0 = unit_entry(A, x, 2 * t + 2);
             e1 = unit_entry(A, x, 2 * t + 3);
             const bool with_q = t == p.t0;
-            const int count = with_q ? 5 + kQPairs : 5;
+            const int count = with_q ? 2 * kQPairs : kQPairs;
 #pragma unroll 1
-            for (int i = 0; i < count; ++i, ++ent) {
-              const bool last = i + 1 == count;
-              if (with_q && last && par == 0) {
-                // the rope dims of Q, once the piece before no longer reads its own
-                if (pieces > 0 && !(ok = wait1(ctl.q_free, (pieces - 1) & 1, abort_flag, err)))
-                  break;
-                mbar_expect_tx(smem_u32(&ctl.rope_full), kAtom);
-                tma_load_2d(smem_u32(sl.q_rope), &tm_q, smem_u32(&ctl.rope_full), 512, q_row);
-                ++ropes;
-              }
-              if ((ent & 1) != par) continue;
-              const int st = ent & (kRing - 1);
-              if (ent >= kRing &&
-                  !(ok = wait1(ctl.k_empty[st], (ent / kRing + 1) & 1, abort_flag, err)))
+            for (int i = par; i < count; i += 2) {
+              const int at = ent + i, st = at & (kRing - 1);
+              if (at >= kRing &&
+                  !(ok = wait1(ctl.k_empty[st], (at / kRing + 1) & 1, abort_flag, err)))
                 break;
+              loaded = at + 1;
               const uint32_t full = smem_u32(&ctl.k_full[st]), dst = smem_u32(sl.ring[st]);
               const int ch = 2 * (with_q ? i >> 1 : i);           // first 64-dim chunk
-              if (with_q && !last && !(i & 1)) {
-                mbar_expect_tx(full, kEntry);
+              mbar_expect_tx(full, with_q && par == 0 ? kEntry : 2 * n * kUnitAtom);
+              if (with_q && par == 0) {
                 tma_load_2d(dst, &tm_q, full, 64 * ch, q_row);
                 tma_load_2d(dst + kAtom, &tm_q, full, 64 * ch + 64, q_row);
               } else {
-                mbar_expect_tx(full, (last ? 1 : 2) * n * kUnitAtom);
                 tma_load_3d(dst, &tm_k, full, 0, c0, ch);
                 if (n > 1) tma_load_3d(dst + kUnitAtom, &tm_k, full, 0, c1, ch);
-                if (!last) {
-                  tma_load_3d(dst + kAtom, &tm_k, full, 0, c0, ch + 1);
-                  if (n > 1) tma_load_3d(dst + kAtom + kUnitAtom, &tm_k, full, 0, c1, ch + 1);
-                }
+                tma_load_3d(dst + kAtom, &tm_k, full, 0, c0, ch + 1);
+                if (n > 1) tma_load_3d(dst + kAtom + kUnitAtom, &tm_k, full, 0, c1, ch + 1);
               }
+            }
+            if (!ok) break;
+            ent += count;
+            if (par == 0 && with_q) {
+              // the rope dims of Q, once the piece before no longer reads its own
+              if (pieces > 0 && !(ok = wait1(ctl.q_free, (pieces - 1) & 1, abort_flag, err))) break;
+              mbar_expect_tx(smem_u32(&ctl.rope_full), kAtom);
+              tma_load_2d(smem_u32(sl.q_rope), &tm_q, smem_u32(&ctl.rope_full), 512, q_row);
+              ++ropes;
+            } else if (par == 1) {
+              // and of K
+              if (ropes > 0 && !(ok = wait1(ctl.kr_empty, (ropes - 1) & 1, abort_flag, err))) break;
+              const uint32_t full = smem_u32(&ctl.kr_full), dst = smem_u32(sl.k_rope);
+              mbar_expect_tx(full, n * kUnitAtom);
+              tma_load_3d(dst, &tm_k, full, 0, c0, 2 * kQPairs);
+              if (n > 1) tma_load_3d(dst + kUnitAtom, &tm_k, full, 0, c1, 2 * kQPairs);
+              ++ropes;
             }
           }
         }
         if (!ok) {           // let the loads in flight land before this CTA leaves
-          for (int c = max(0, ent - kRing); c < ent; ++c)
+          for (int c = max(0, loaded - kRing); c < loaded; ++c)
             if ((c & 1) == par)
               mbar_drain(smem_u32(&ctl.k_full[c & (kRing - 1)]), (c / kRing) & 1);
-          if (ropes > 0) mbar_drain(smem_u32(&ctl.rope_full), (ropes - 1) & 1);
+          if (ropes > 0)
+            mbar_drain(smem_u32(par == 0 ? &ctl.rope_full : &ctl.kr_full), (ropes - 1) & 1);
         }
       }
     } else if (warp >= 12) {
@@ -506,7 +519,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl.q_ready[j]));
         }
-        ent += 5 * (p.t1 - p.t0) + kQPairs;
+        ent += kQPairs * (p.t1 - p.t0 + 1);
       }
     } else if (warp == 1) {
       // ------------------------------------------------------- QK (CTA 0)
@@ -517,6 +530,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t id2 = idesc_bf16(128, 128, false), id1 = idesc_bf16(128, 64, false);
         const uint64_t ring_d = sdesc_sw128(smem_u32(sl.ring[0]), 0, 1024);
         const uint64_t rope_d = sdesc_sw128(smem_u32(sl.q_rope), 0, 1024);
+        const uint64_t kr_d = sdesc_sw128(smem_u32(sl.k_rope), 0, 1024);
         const uint32_t k_full = smem_u32(&ctl.k_full[0]), k_empty = smem_u32(&ctl.k_empty[0]);
         int ent = 0, tc = 0;
         auto ask = [&](int e) {
@@ -548,7 +562,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tc_fence_after();
               }
               if (!(ok = full(ent, there))) break;
-              there = (!first || j + 1 == kQPairs) && ask(ent + 1);
+              there = !first && j + 1 < kQPairs && ask(ent + 1);
               const int st = ent & (kRing - 1);
               const uint64_t kd = ring_d + st * (kEntry >> 4);
               const uint32_t qc = tmem + kColQ + 64 * j;
@@ -560,17 +574,14 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             if (!ok) break;
             if (first && !(ok = wait1(ctl.rope_full, pieces & 1, abort_flag, err))) break;
-            if (!(ok = full(ent, there))) break;
+            if (!(ok = wait1(ctl.kr_full, tc & 1, abort_flag, err))) break;
             room = tc == 0 || mbar_try_wait(smem_u32(&ctl.s_empty[sb ^ 1]),
                                             (((tc + 1) >> 1) + 1) & 1);
-            const int st = ent & (kRing - 1);
-            const uint64_t kd = ring_d + st * (kEntry >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) mma_bf16(d, rope_d + 2 * kk, kd + 2 * kk, id, 1u);
-            mma_commit(k_empty + 8 * st);
+            for (int kk = 0; kk < 4; ++kk) mma_bf16(d, rope_d + 2 * kk, kr_d + 2 * kk, id, 1u);
+            mma_commit(smem_u32(&ctl.kr_empty));
             mma_commit(smem_u32(&ctl.s_full[sb]));
             if (t + 1 == p.t1) mma_commit(smem_u32(&ctl.q_free));
-            ++ent;
           }
         }
         if (!ok) {           // MMAs in flight read shared memory: wait for them
@@ -599,9 +610,9 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               // or a later one's, and PV waits for its tile's rescale.
               if (u == 0)
                 bulk_copy_to_peer(mapa(smem_u32(so.alpha[tc & 3]), peer), smem_u32(sl.alpha[g]),
-                                  512, mapa(smem_u32(&ctl.al_full[tc & 3]), peer));
+                                  512, mapa(smem_u32(&so.al_full[tc & 3]), peer));
               bulk_copy_to_peer(mapa(smem_u32(so.p[slot]), peer), smem_u32(sl.p[g][u]), kAtom,
-                                mapa(smem_u32(&ctl.p_full[slot]), peer));
+                                mapa(smem_u32(&so.p_full[slot]), peer));
               sent ^= 1u << bit;
             }
           }
@@ -702,12 +713,15 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               }
             }
             if (round == 1) break;
-            // the row's maximum over both units
-            sl.mx[b][g][r] = mx;
+            // the row's maximum over both units; the other group has read the
+            // tile before's once it is done with its logits
+            if (tc > 0 && !(ok = wait32(ctl.s_empty[b ^ 1], ((tc - 1) >> 1) & 1, abort_flag, err)))
+              break;
+            sl.mx[g][r] = mx;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&ctl.mx_bar[wq]));
             if (!(ok = wait32(ctl.mx_bar[wq], tc & 1, abort_flag, err))) break;
-            const float top = fmaxf(mx, sl.mx[b][g ^ 1][r]) * A.sm_scale_log2;
+            const float top = fmaxf(mx, sl.mx[g ^ 1][r]) * A.sm_scale_log2;
             const float m_new = top > m + kRebase ? top : m;
             const bool moved = m_new != m;
             if (moved && m > -INFINITY) alpha = fast_exp2(m - m_new);
@@ -733,7 +747,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         st_cluster_f32(ml, m);
         st_cluster_f32(ml + 4, l);
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctl.ml_full), peer));
+        if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&so.ml_full), peer));
       }
     }
   } else {
@@ -752,9 +766,9 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int h = 0; h < 2 * n; ++h, ++vc) {
               const int st = vc & 3;
               if (vc >= kVRing &&
-                  !(ok = wait1(ctl.v_empty[st], ((vc >> 2) + 1) & 1, abort_flag, err)))
+                  !(ok = wait1(so.v_empty[st], ((vc >> 2) + 1) & 1, abort_flag, err)))
                 break;
-              const uint32_t full = smem_u32(&ctl.v_full[st]);
+              const uint32_t full = smem_u32(&so.v_full[st]);
               mbar_expect_tx(full, kVChunk);
               tma_load_3d(smem_u32(so.v[st]), &tm_v, full, 0, h < 2 ? c0 : c1, 4 * (h & 1));
             }
@@ -762,7 +776,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         if (!ok)
           for (int c = max(0, vc - kVRing); c < vc; ++c)
-            mbar_drain(smem_u32(&ctl.v_full[c & 3]), (c >> 2) & 1);
+            mbar_drain(smem_u32(&so.v_full[c & 3]), (c >> 2) & 1);
       }
     } else if (warp == 1) {
       // ------------------------------------------------------- PV (CTA 1)
@@ -776,30 +790,30 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (; next_piece(false); ++pieces) {
           for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
             const int n = tile_units(x, t);
-            if (!(ok = wait1(ctl.o_ok[tc & 3], (tc >> 2) & 1, abort_flag, err))) break;
+            if (!(ok = wait1(so.o_ok[tc & 3], (tc >> 2) & 1, abort_flag, err))) break;
             tc_fence_after();
             for (int u = 0; ok && u < n; ++u, ++ac) {
               const int slot = ac & 3;
-              if (!(ok = wait1<true>(ctl.p_full[slot], (ac >> 2) & 1, abort_flag, err))) break;
+              if (!(ok = wait1<true>(so.p_full[slot], (ac >> 2) & 1, abort_flag, err))) break;
               if (2 * t + u < x.nu && unit_hidden(A, x, 2 * t + u) != 0ull) {
-                if (!(ok = wait1(ctl.clean[u], (cleaned >> u) & 1, abort_flag, err))) break;
+                if (!(ok = wait1(so.clean[u], (cleaned >> u) & 1, abort_flag, err))) break;
                 cleaned ^= 1u << u;
               }
               const uint64_t pd = p_d + slot * (kAtom >> 4);
 #pragma unroll 1
               for (int h = 0; h < 2; ++h, ++vc) {
                 const int st = vc & 3;
-                if (!(ok = wait1(ctl.v_full[st], (vc >> 2) & 1, abort_flag, err))) break;
+                if (!(ok = wait1(so.v_full[st], (vc >> 2) & 1, abort_flag, err))) break;
                 const uint64_t vd = v_d + st * (kVChunk >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)          // 16 keys: 32 B of P, 2 KB of V
                   mma_bf16(tmem + 256 * h, pd + 2 * kk, vd + (kk * 2048 >> 4), id,
                            (t > p.t0 || u > 0 || kk > 0) ? 1u : 0u);
-                mma_commit(smem_u32(&ctl.v_empty[st]));
+                mma_commit(smem_u32(&so.v_empty[st]));
               }
-              mma_commit(smem_u32(&ctl.p_free[slot]));
+              mma_commit(smem_u32(&so.p_free[slot]));
             }
-            mma_commit(smem_u32(&ctl.pv_done[tc & 3]));
+            mma_commit(smem_u32(&so.pv_done[tc & 3]));
           }
           mma_commit(smem_u32(&ctl.o_done));
         }
@@ -821,13 +835,13 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               const int slot = a & 3;
               if (warp == 2) {
                 if (u == 0 &&
-                    !(ok = wait1<true>(ctl.al_full[tc & 3], (tc >> 2) & 1, abort_flag, err)))
+                    !(ok = wait1<true>(so.al_full[tc & 3], (tc >> 2) & 1, abort_flag, err)))
                   break;
-                if (!(ok = wait1<true>(ctl.p_full[slot], (a >> 2) & 1, abort_flag, err))) break;
+                if (!(ok = wait1<true>(so.p_full[slot], (a >> 2) & 1, abort_flag, err))) break;
                 mbar_arrive_remote(mapa(smem_u32(&ctl.p_ack[tc & 1][u]), peer));
               } else {
-                if (!(ok = wait1(ctl.p_free[slot], (a >> 2) & 1, abort_flag, err))) break;
-                mbar_expect_tx(smem_u32(&ctl.p_full[slot]), kAtom);
+                if (!(ok = wait1(so.p_free[slot], (a >> 2) & 1, abort_flag, err))) break;
+                mbar_expect_tx(smem_u32(&so.p_full[slot]), kAtom);
                 mbar_arrive_remote(mapa(smem_u32(&ctl.p_room[slot]), peer));
               }
             }
@@ -842,7 +856,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       // has at least one.
       for (pieces = 1; p.item >= 0; ++pieces) {
         const int done = pieces - kPieces / 2;
-        if (!(ok = ok && (done < 0 || wait32(ctl.piece_done[done & (kPieces - 1)],
+        if (!(ok = ok && (done < 0 || wait32(so.piece_done[done & (kPieces - 1)],
                                              (done / kPieces) & 1, abort_flag, err))))
           break;
         p = walk.next(A);
@@ -871,12 +885,12 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
           const int n = tile_units(x, t);
           const int sl4 = tc & 3;
-          if (!(ok = wait32<true>(ctl.al_full[sl4], (tc >> 2) & 1, abort_flag, err))) break;
-          if (threadIdx.x == 128) mbar_expect_tx(smem_u32(&ctl.al_full[sl4]), 512);
+          if (!(ok = wait32<true>(so.al_full[sl4], (tc >> 2) & 1, abort_flag, err))) break;
+          if (threadIdx.x == 128) mbar_expect_tx(smem_u32(&so.al_full[sl4]), 512);
           const float alpha = so.alpha[sl4][r];
           if (__any_sync(0xffffffffu, alpha != 1.f)) {
             // never on a piece's first tile, so the PV of the tile before is this piece's
-            if (!(ok = wait32(ctl.pv_done[(tc + 3) & 3], ((tc - 1) >> 2) & 1, abort_flag, err)))
+            if (!(ok = wait32(so.pv_done[(tc + 3) & 3], ((tc - 1) >> 2) & 1, abort_flag, err)))
               break;
             tc_fence_after();
 #pragma unroll 1
@@ -890,7 +904,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl.o_ok[sl4]));
+          if (lane == 0) mbar_arrive(smem_u32(&so.o_ok[sl4]));
           // Keys that some row does not see have zeros in its P, and a zero
           // times a NaN or infinite value would reach that row: such values
           // become 0 (a row that sees them has a NaN logit). PV of this unit
@@ -901,14 +915,14 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (hidden == 0ull) continue;
             // once the tile before is done, its chunks' barriers are in the
             // phase before the one waited for
-            if (t > p.t0 && !(ok = wait32(ctl.pv_done[(tc + 3) & 3], ((tc - 1) >> 2) & 1,
+            if (t > p.t0 && !(ok = wait32(so.pv_done[(tc + 3) & 3], ((tc - 1) >> 2) & 1,
                                           abort_flag, err)))
               break;
             const int k0 = __ffsll(static_cast<long long>(hidden)) - 1;
             const int k1 = 64 - __clzll(static_cast<long long>(hidden));
             for (int h = 0; h < 2; ++h) {
               const int c = vc + h;
-              if (!(ok = wait32(ctl.v_full[c & 3], (c >> 2) & 1, abort_flag, err))) break;
+              if (!(ok = wait32(so.v_full[c & 3], (c >> 2) & 1, abort_flag, err))) break;
               auto clean = [](uint32_t w) {
                 if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
                 if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
@@ -929,12 +943,12 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (!ok) break;
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&ctl.clean[u]));
+            if (lane == 0) mbar_arrive(smem_u32(&so.clean[u]));
           }
         }
         if (!ok) break;
         // ------------------------------------------------------- a piece's end
-        if (!(ok = wait32<true>(ctl.ml_full, pieces & 1, abort_flag, err))) break;
+        if (!(ok = wait32<true>(so.ml_full, pieces & 1, abort_flag, err))) break;
         const float2 a0 = so.ml[0][r], a1 = so.ml[1][r];
         __syncwarp();
         if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctl.ml_free), peer));
@@ -1008,7 +1022,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
         if (threadIdx.x == 128)
-          mbar_arrive(smem_u32(&ctl.piece_done[pieces & (kPieces - 1)]));
+          mbar_arrive(smem_u32(&so.piece_done[pieces & (kPieces - 1)]));
       }
       if (threadIdx.x == 128 && !recorded && A.rec) A.rec[cluster] = make_int2(-1, 0);
     }
