@@ -42,13 +42,14 @@
 //
 // What bounds it. A tile's MMAs take CTA 0 2400 cycles and CTA 1 2050, and CTA
 // 0's shared memory takes 368 KB a tile in and out (K in and to the MMA, the rope
-// dims of Q, P in and out), 2900 cycles at 128 B each. Measured, a tile takes some
-// 3500 cycles with the cache in L2 (64 sequences of 32768 tokens that share 37 MB:
-// 472 us) and 4100 from HBM (595 us, 4.1 TB/s), where QK waits for K. That run is
-// held at 1.5 GHz of 1.97 by the board's 1000 W; short calls run at full clock, and
-// their time is the way to the first tile (9 us), the shares' tiles (2 to 2.3 us
-// each), a part's way to memory (5 us: an SM writes some 30 B a cycle) and the join
-// (7 us): one sequence of 131072 tokens 62 us.
+// dims of Q, P in and out), 2900 cycles at 128 B each. Measured, a tile takes 3400
+// cycles with the cache in L2 (64 sequences of 32768 tokens that share 37 MB: 472
+// us), where the softmax's 2700 and its waits set the pace and QK waits 450 for a
+// buffer, and 3850 from HBM (595 us, 4.1 TB/s), where QK waits 1000 for K. That run
+// is held at 1.5 GHz of 1.97 by the board's 1000 W; short calls run at full clock,
+// and their time is the way to the first tile (9 us), the shares' tiles (2 to 2.3
+// us each), a part's way to memory (5 us: an SM writes some 30 B a cycle) and the
+// join (7 us): one sequence of 131072 tokens 62 us.
 //
 // CTA 0's shared memory is full to the last bytes. The rope dims of K in a place of
 // their own, not in the ring, took 64 x 32768 from 635 to 595 us; what paid for
@@ -277,7 +278,7 @@ struct Ctl {
   unsigned long long p_ack[2][2];               // CTA 1 holds the atom: its staging is free
   unsigned long long p_room[kPSlots];           // CTA 1 has room for another atom
   unsigned long long ml_free;                   // CTA 1 has read ml
-  unsigned long long o_done;
+  unsigned long long o_done;                    // CTA 1's PV of a piece; the give-up path
   Share share;                                  // of the row tiles' weights
   unsigned long long piece_full[kPieces];
   uint32_t tmem_base;
@@ -307,8 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v,
                  const __grid_constant__ RangeArgs A) {
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* big = smem_raw;
+  extern __shared__ __align__(1024) uint8_t big[];              // (swizzled tiles start on 1024 B)
   LogitsSmem& sl = *reinterpret_cast<LogitsSmem*>(big);
   OutputSmem& so = *reinterpret_cast<OutputSmem*>(big);
   Ctl& ctl = *reinterpret_cast<Ctl*>(big + kBig);
