@@ -59,6 +59,7 @@
 // it was 508; one a unit and five ring entries: 707), and entries of 16 KB cost a
 // wait and a commit more each (598 us).
 #include <algorithm>
+#include <cstddef>
 
 #include "common.cuh"
 #include "dsa_internal.h"
@@ -116,6 +117,17 @@ struct OutputSmem {                             // CTA 1
 };
 constexpr size_t kBig = std::max(sizeof(LogitsSmem), sizeof(OutputSmem));
 static_assert(kBig % 1024 == 0, "the control block follows the larger role's memory");
+// Scratch of the search for the share. It may still run in CTA 1 when CTA 0's
+// first atoms of P arrive (the cluster's barrier is passed on arrival, before the
+// search), so it lies where no copy or load lands in either CTA: CTA 1's staging
+// of output rows, and at the same place in CTA 0 a staging of P, which only that
+// CTA's softmax writes, after the search.
+constexpr size_t kScratch = offsetof(OutputSmem, stage);
+constexpr size_t kScratchBytes = 2 * (kThreads / 32) * sizeof(long long);
+static_assert(kScratchBytes <= sizeof(OutputSmem::stage) && kScratch % 8 == 0 &&
+                  kScratch >= offsetof(LogitsSmem, p) &&
+                  kScratch + kScratchBytes <= offsetof(LogitsSmem, q_rope),
+              "the search's scratch is out of reach of copies and loads");
 
 // The bits a .. b of 0 .. 63 (none if a > b).
 __device__ __forceinline__ unsigned long long range_bits(int a, int b) {
@@ -373,7 +385,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       ctl.share.whole = 1;
     }
   } else {
-    find_share<kThreads>(ctl.share, reinterpret_cast<long long*>(big), A.items, cluster,
+    find_share<kThreads>(ctl.share, reinterpret_cast<long long*>(big + kScratch), A.items, cluster,
                          A.clusters, A.items < A.clusters ? kCutCostFew : kCutCostMany,
                          [&](int i) {
                            if (A.block_table && blockIdx.x == 0) {
@@ -383,7 +395,6 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                            return item_geom(A, i).tiles + kItemCost;
                          });
   }
-  fence_proxy_async_smem();               // find_share's scratch, before loads land there
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
