@@ -561,7 +561,11 @@ int dsa_attention_mass_paged(const void *q, const void *kv_pool, const int32_t *
  *                 overlap it; ld_out >= min(budget, 64 * max_blocks); entries
  *                 past the new length are not written
  * Rows past the new length keep their bytes. A block id outside [0, nblk) is
- * recorded as DSA_ERR_DEVICE_BOUNDS and the rows it holds do not move.
+ * recorded as DSA_ERR_DEVICE_BOUNDS and the rows it holds do not move. A
+ * timeout that is pending when a sequence's selection begins (see
+ * dsa_get_device_error) leaves everything of that sequence as it is, outputs
+ * included; one that another stream records or clears later changes nothing,
+ * so a sequence is evicted as a whole or not at all.
  * B at most 65535 (DSA_ERR_UNSUPPORTED).
  */
 int dsa_cache_evict_paged(void *kv_pool, void *k8_pool, float *k_scale_pool,

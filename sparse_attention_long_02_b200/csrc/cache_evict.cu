@@ -28,6 +28,13 @@
 // HBM, each moved byte read and written once (64 x 32768 -> 16384 tokens: 481 us
 // with the selection, 5.6 TB/s), and for few sequences by the latency of a step's
 // chain (read, barrier, write).
+//
+// A pending timeout (of this or another stream) leaves a sequence as it is. The
+// selection alone looks at the error word, which other streams may set and clear
+// at any time, and leaves a verdict for each sequence that all CTAs of the move
+// obey: a sequence is evicted as a whole or not at all.
+#include <atomic>
+
 #include "common.cuh"
 #include "dsa_internal.h"
 
@@ -43,6 +50,19 @@ constexpr int kBins = 2048;
 constexpr int kMoveThreads = 1024;
 constexpr int kDepth = 3;                       // steps of a move in shared memory
 constexpr int kMoveWant = 256, kMoveMost = 296; // CTAs that move latent rows, at least and at most
+
+// A call's verdicts, a byte a sequence: its place in the list of eager calls or of
+// captured ones, which are launched again later. Two calls share a place only with
+// a million sequences between them, and then must run at the same time, with a
+// timeout set or cleared between their selections, for one to read the other's.
+constexpr unsigned kVerdicts = 1u << 20;
+__device__ unsigned char g_verdict[2][kVerdicts];
+struct Verdicts {
+  unsigned list, first;
+  __device__ __forceinline__ unsigned char& of(int b) const {
+    return g_verdict[list][(first + static_cast<unsigned>(b)) & (kVerdicts - 1)];
+  }
+};
 
 // Order-preserving key of a total; NaN below everything, -0 equal to +0.
 __device__ __forceinline__ unsigned total_key(float v) {
@@ -82,7 +102,8 @@ __device__ __forceinline__ unsigned sum_from_lane(unsigned x) {
   return x;
 }
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictArgs A) {
+__global__ void __launch_bounds__(kSelThreads)
+evict_select_kernel(const EvictArgs A, const Verdicts verdicts) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   SelSmem& sm = *reinterpret_cast<SelSmem*>(smem_raw);
   unsigned* kept_keys = reinterpret_cast<unsigned*>(smem_raw + sizeof(SelSmem));
@@ -94,7 +115,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictAr
   int* idx = A.idx + static_cast<long long>(b) * A.budget;
   if (tid == 0) sm.skip = launch_aborted(A.err);
   cluster_sync();                               // also: seq_len_out may be seq_len
-  if (ld_cluster(mapa(smem_u32(&sm.skip), 0))) {
+  const bool skip = ld_cluster(mapa(smem_u32(&sm.skip), 0)) != 0;
+  if (rank == 0 && tid == 0) verdicts.of(b) = !skip;
+  if (skip) {
     cluster_sync();
     return;
   }
@@ -287,11 +310,11 @@ __device__ __forceinline__ void move_columns(const EvictArgs& A, MoveSmem& sm, i
   const int* idx = A.idx + static_cast<long long>(b) * A.budget;
   const int* table = A.block_table + static_cast<long long>(b) * A.max_blocks;
   // (the last kept row in its place: so are all before it)
-  if (from == to && (count == 0 || __ldg(idx + count - 1) == count - 1)) return;
+  if (count <= 0 || (from == to && __ldg(idx + count - 1) == count - 1)) return;
   int src, slot, src_block, dst_block;
   auto slots = [&](int j) { src = j < end ? __ldg(idx + j) : -1; };
   auto blocks = [&](int j) {
-    const bool moves = src >= 0 && !(src == j && from == to);
+    const bool moves = src >= 0 && src < A.max_blocks * 64 && !(src == j && from == to);
     slot = moves ? src : -1;
     src_block = moves && paged ? __ldg(table + (src >> 6)) : 0;
     dst_block = moves && paged ? __ldg(table + (j >> 6)) : 0;
@@ -343,12 +366,13 @@ __device__ __forceinline__ void move_columns(const EvictArgs& A, MoveSmem& sm, i
 
 // Job y of a sequence: a slice of the latent rows' 72 16-byte columns, then the
 // indexer's keys, their scales and the totals.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictArgs A, int slices) {
+__global__ void __launch_bounds__(kMoveThreads)
+evict_move_kernel(const EvictArgs A, const Verdicts verdicts, int slices) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   MoveSmem& sm = *reinterpret_cast<MoveSmem*>(smem_raw);
   const int b = static_cast<int>(blockIdx.x / cluster_size());
-  if (__syncthreads_or(launch_aborted(A.err))) return;
-  const int count = A.seq_len_out[b];
+  const int count = min(A.seq_len_out[b], min(A.budget, A.max_blocks * 64));
+  if (!verdicts.of(b)) return;                  // (the same for all CTAs of the sequence)
   const int job = static_cast<int>(blockIdx.y);
   if (job < slices) {
     uint4* p = static_cast<uint4*>(A.kv_pool);
@@ -388,7 +412,14 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+  static std::atomic<unsigned> next[2];
+  cudaStreamCaptureStatus capture;
+  e = cudaStreamIsCapturing(st, &capture);
+  if (e != cudaSuccess) return e;
+  Verdicts verdicts;
+  verdicts.list = capture == cudaStreamCaptureStatusNone ? 0 : 1;
+  verdicts.first = next[verdicts.list].fetch_add(static_cast<unsigned>(a.B));
+  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, verdicts);
   if (e != cudaSuccess) return e;
   // Whole rows where the sequences' clusters fill the GPU, else as few slices of
   // them as do, of 384, 128 or 64 bytes (measured with 512 threads a CTA, 64 x
@@ -405,7 +436,7 @@ cudaError_t launch_cache_evict(const EvictArgs& a, cudaStream_t st) {
   e = cudaFuncSetAttribute(evict_move_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(cfg.dynamicSmemBytes));
   if (e != cudaSuccess) return e;
-  return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, slices);
+  return cudaLaunchKernelEx(&cfg, evict_move_kernel, a, verdicts, slices);
 }
 
 }  // namespace dsa

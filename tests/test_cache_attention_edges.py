@@ -51,3 +51,98 @@ def test_decode_of_thousands_of_short_sequences(dsa, B, nq, H, most, window):  #
         n = lens[b]
         see = np.stack([sees(n - nq + j, n, 3, window) for j in range(nq)]).repeat(H, 0)
         check_rows(out[b].view(-1, 512), lse[b].view(-1), q[b].view(-1, 576), seq_rows(c, b), see)
+
+
+# ------------------------------------- a call cut between its two launches
+
+class Halves:
+    """A captured call of two launches that can be replayed one launch at a time."""
+
+    def __init__(self, call):
+        from cuda.bindings import driver
+        self.drv = driver
+        call()                                          # what is set up once, outside the capture
+        torch.cuda.synchronize()
+        self.graph = torch.cuda.CUDAGraph(keep_graph=True)
+        with torch.cuda.graph(self.graph):
+            call()
+        raw = driver.CUgraph(self.graph.raw_cuda_graph())
+        n = self._do(driver.cuGraphGetNodes(raw))[1]
+        nodes = self._do(driver.cuGraphGetNodes(raw, n))[0]
+        root = self._do(driver.cuGraphGetRootNodes(raw, 1))[0][0]
+        assert n == 2
+        self.nodes = sorted(nodes, key=lambda k: int(k) != int(root))
+        self.exe = self._do(driver.cuGraphInstantiate(raw, 0))[0]
+
+    def _do(self, result):
+        assert result[0] == self.drv.CUresult.CUDA_SUCCESS, result[0]
+        return result[1:]
+
+    def run(self, half):
+        for i, node in enumerate(self.nodes):
+            self._do(self.drv.cuGraphNodeSetEnabled(self.exe, node, int(i == half)))
+        self._do(self.drv.cuGraphLaunch(self.exe, torch.cuda.current_stream().cuda_stream))
+        torch.cuda.synchronize()
+
+    def close(self):
+        self._do(self.drv.cuGraphExecDestroy(self.exe))
+        self.graph.reset()
+
+
+def leave_a_timeout(dsa):  # noqa: F811
+    """A pending timeout: a bounded wait (1 s) that nothing arrives at runs out."""
+    kv = torch.zeros(1, 64, 576, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(1, 1, 8, 576, dtype=torch.bfloat16, device="cuda")
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    dsa.debug_stall(dsa.DEBUG_STALL_MLA)
+    try:
+        dsa.split_mla_decode_paged(q, kv, torch.zeros(1, 1, dtype=torch.int32, device="cuda"), one,
+                                   SM)
+        torch.cuda.synchronize()
+    finally:
+        dsa.debug_stall(0)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B", [1, 40])
+def test_an_eviction_is_done_as_a_whole_or_not_at_all(dsa, B, in_place):  # noqa: F811
+    """Between the selection and the move another stream's caller clears the timeout
+    that the selection met, or another stream's kernel records one."""
+    lens, budget = [900 - 7 * (b % 9) for b in range(B)], 300
+    c = packed_cache(lens, 60 + B)
+    mass = torch.rand(B, c["block_table"].shape[1] * 64, generator=c["g"], device="cuda")
+    idx = torch.empty(B, budget, dtype=torch.int32, device="cuda")
+    new = c["seq_len"] if in_place else torch.empty_like(c["seq_len"])
+    mout = mass if in_place else torch.empty_like(mass)
+    state = [c["kv_pool"], c["seq_len"], mass, idx, new, mout]
+
+    def call():
+        dsa.cache_evict_paged(c["kv_pool"], c["block_table"], c["seq_len"], mass, budget, 4, 50,
+                              idx=idx, seq_len_out=new, mass_out=mout)
+
+    idx.zero_(), new.copy_(c["seq_len"]), mout.copy_(mass)
+    start = [t.clone() for t in state]
+    halves = Halves(call)
+    done = [t.clone() for t in state]                   # what one whole call makes of it
+    for t, s in zip(state, start):
+        t.copy_(s)
+    # outputs that look like those of an earlier call
+    idx.copy_(torch.arange(budget, device="cuda").expand(B, -1) * 2)
+    if not in_place:
+        new.fill_(budget)
+    held = [t.clone() for t in state]
+    no_device_error(dsa)
+    leave_a_timeout(dsa)
+    halves.run(0)
+    assert dsa.get_device_error() == -5                 # read, and cleared, by somebody else
+    halves.run(1)
+    no_device_error(dsa)
+    for t, h in zip(state, held):
+        assert torch.equal(t, h)
+    halves.run(0)
+    leave_a_timeout(dsa)
+    halves.run(1)
+    assert dsa.get_device_error() == -5
+    for t, d in zip(state, done):
+        assert torch.equal(t, d)
+    halves.close()
