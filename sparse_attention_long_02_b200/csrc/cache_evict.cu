@@ -126,8 +126,10 @@ evict_select_kernel(const EvictArgs A, const Verdicts verdicts) {
     A.seq_len_out[b] = min(n, A.budget);
   }
   if (n <= A.budget) {
-    for (int i = rank * kSelThreads + tid; i < A.budget; i += cl * kSelThreads)
-      idx[i] = i < n ? i : -1;
+    // (unsigned: a budget of no limit is near 2^31)
+    for (unsigned i = rank * kSelThreads + tid; i < static_cast<unsigned>(A.budget);
+         i += cl * kSelThreads)
+      idx[i] = i < static_cast<unsigned>(n) ? static_cast<int>(i) : -1;
     cluster_sync();                             // the others may still read sm.skip
     return;
   }

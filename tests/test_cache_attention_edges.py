@@ -146,3 +146,24 @@ def test_an_eviction_is_done_as_a_whole_or_not_at_all(dsa, B, in_place):  # noqa
     for t, d in zip(state, done):
         assert torch.equal(t, d)
     halves.close()
+
+
+# ----------------------------------------------------------- largest counts
+
+def test_evict_with_a_budget_of_no_limit(dsa):  # noqa: F811
+    """The largest budget the interface takes: all is kept, and its row of slots ends
+    where it should."""
+    c = packed_cache([700], 90)
+    mass = torch.rand(1, 704, generator=c["g"], device="cuda")
+    kv, budget = c["kv_pool"].clone(), 2 ** 31 - 1
+    buf = torch.zeros(budget + 65, dtype=torch.int32, device="cuda")
+    idx = buf[32:32 + budget].view(1, budget)
+    _, new, mout = dsa.cache_evict_paged(c["kv_pool"], c["block_table"], c["seq_len"], mass, budget,
+                                         4, 100, idx=idx)
+    no_device_error(dsa)
+    assert new.tolist() == [700] and torch.equal(c["kv_pool"], kv)
+    assert torch.equal(mout[:, :700], mass[:, :700])
+    assert idx[0, :700].tolist() == list(range(700))
+    for part in idx[0, 700:].split(1 << 28):
+        assert int(part.max()) == -1 and int(part.min()) == -1
+    assert not buf[:32].any() and not buf[32 + budget:].any()
