@@ -1048,15 +1048,17 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 // Joins the parts of the cut row tiles. Record c names the row tile whose first
-// tile closes cluster c's share. A task is 32 rows and 128 value dims of a row
-// tile, 16 dims a warp; where the row tile has many parts, 8 dims, whose parts
-// the eight warps share. The weights are worked out once a task. A warp reads
-// 512 consecutive bytes at a time (four dims of 32 rows), eight reads in
-// flight, the first of them asked for before the weights are known. Bound by
-// the latency of a task's chain (record, maxima, weights, sums), so tasks are
-// few and large: one sequence of 131072 tokens, 73 parts of 256 KB, 7 us with the
-// launch (13 us in tasks of 32 dims with the weights worked out for each); 33
-// sequences of up to 32768, two queries each, 9 us (20 us).
+// tile closes cluster c's share; a cluster that ran nothing, or gave up before it
+// wrote a first part, leaves none. So the error word, which other streams set and
+// clear, is not looked at here: what the first launch wrote is joined. A task is
+// 32 rows and 128 value dims of a row tile, 16 dims a warp; where the row tile has
+// many parts, 8 dims, whose parts the eight warps share. The weights are worked
+// out once a task. A warp reads 512 consecutive bytes at a time (four dims of 32
+// rows), eight reads in flight, the first of them asked for before the weights are
+// known. Bound by the latency of a task's chain (record, maxima, weights, sums), so
+// tasks are few and large: one sequence of 131072 tokens, 73 parts of 256 KB, 7 us
+// with the launch (13 us in tasks of 32 dims with the weights worked out for each);
+// 33 sequences of up to 32768, two queries each, 9 us (20 us).
 constexpr int kJoinThreads = 256, kJoinResident = 3, kJoinCtas = kJoinResident * 148;
 constexpr int kJoinBatch = (kMaxClusters + 7) / 8;              // parts a warp weighs
 constexpr int kJoinRecs = (kMaxClusters + 31) / 32;             // records a lane looks at
@@ -1173,7 +1175,6 @@ range_join_kernel(const __grid_constant__ RangeArgs A) {
     item[k] = rec.x;
     parts[k] = rec.y - c + 1;                   // slot 1 of c, slot 0 of c+1 .. rec.y
   }
-  const bool skip = launch_aborted(A.err);
 #pragma unroll
   for (int k = 0; k < kJoinRecs; ++k)
     if (item[k] >= 0) tasks += join_tasks(parts[k]) * row_blocks;
@@ -1184,7 +1185,6 @@ range_join_kernel(const __grid_constant__ RangeArgs A) {
     if (lane >= o) end += y;
   }
   const int total = __shfl_sync(0xffffffffu, end, 31);
-  if (__syncthreads_or(skip)) return;
   for (int task = static_cast<int>(blockIdx.x); task < total; task += kJoinCtas) {
     const int owner = __ffs(__ballot_sync(0xffffffffu, task < end)) - 1;
     int at = task - (end - tasks), c = 0, it = 0, n = 0;

@@ -167,3 +167,34 @@ def test_evict_with_a_budget_of_no_limit(dsa):  # noqa: F811
     for part in idx[0, 700:].split(1 << 28):
         assert int(part.max()) == -1 and int(part.min()) == -1
     assert not buf[:32].any() and not buf[32 + budget:].any()
+
+
+def test_a_split_call_is_joined_whatever_the_error_word_says(dsa):  # noqa: F811
+    """Between the shares and their join another stream's kernel records a timeout, or
+    its caller clears the one that the shares met."""
+    lens = [9000, 40, 3001]
+    c = packed_cache(lens, 95)
+    q = randn(c["g"], 3, 1, 128, 576)
+    out = torch.empty(3, 1, 128, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(3, 1, 128, device="cuda")
+    ws = torch.full((dsa.split_mla_decode_workspace_size(3, 1, c["block_table"].shape[1], 128),),
+                    255, dtype=torch.uint8, device="cuda")
+    halves = Halves(lambda: dsa.split_mla_decode_paged(q, c["kv_pool"], c["block_table"],
+                                                       c["seq_len"], SM, out=out, lse=lse,
+                                                       workspace=ws))
+    ref = out.clone(), lse.clone()
+    no_device_error(dsa)
+    out.fill_(7), lse.fill_(7), ws.fill_(255)
+    halves.run(0)
+    leave_a_timeout(dsa)
+    halves.run(1)
+    assert dsa.get_device_error() == -5
+    assert torch.equal(out, ref[0]) and torch.equal(lse, ref[1])
+    out.fill_(7), lse.fill_(7), ws.fill_(255)
+    leave_a_timeout(dsa)
+    halves.run(0)
+    assert dsa.get_device_error() == -5
+    halves.run(1)
+    no_device_error(dsa)
+    assert (out == 7).all() and (lse == 7).all()
+    halves.close()
