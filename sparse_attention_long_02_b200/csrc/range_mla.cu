@@ -106,6 +106,7 @@ struct OutputSmem {                             // CTA 1
   float alpha[4][128];                          // rescale factors, by tile
   float2 ml[2][128];                            // reference maximum and sum of each softmax group
   uint8_t stage[8][32 * 64];                    // output rows on their way out, by warp
+  unsigned lost[128][16];                       // by row, a bit a dim: see clean_v
   unsigned long long v_full[kVRing], v_empty[kVRing];
   unsigned long long p_full[kPSlots], p_free[kPSlots];
   unsigned long long al_full[4];                // a tile's rescale factors have landed
@@ -316,6 +317,70 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// The sign bits of a word's two bf16 that are NaN or infinite.
+__device__ __forceinline__ unsigned not_finite(uint32_t w) {
+  return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+}
+// This thread's 16-byte pieces of a V chunk's rows k0 .. k1 - 1: piece i is of row
+// k0 + i / 4, in atom i % 4 (rows of 128 B, 16-B chunk c of row k at c ^ (k % 8)).
+constexpr int kCleaners = 256;                  // threads
+__device__ __forceinline__ uint4* v_piece(uint8_t* v, int k0, int i, int sub) {
+  return reinterpret_cast<uint4*>(v + (i & 3) * kUnitAtom + (k0 + (i >> 2)) * 128 + (sub & 7) * 16);
+}
+// Turns the NaN and infinite values of those pieces into 0.
+//
+// An infinite value v of a key that a row sees with logit -inf makes p v = 0 inf, a
+// NaN, of that dim of the row; with any other logit the whole row is NaN. So the
+// dims are noted in `lost` for the rows that see the key. `key0` is the key of the
+// chunk's row 0, `dim0` its first dim.
+__device__ __noinline__ void clean_v(const RangeArgs& A, uint8_t* v, int k0, int k1, int sub, int key0,
+                                     int dim0, int pos0, int last, int nrows, unsigned (*lost)[16],
+                                     unsigned long long& o_ok, uint32_t parity,
+                                     volatile int* abort_flag, unsigned* err) {
+  bool ready = false;
+#pragma unroll 1
+  for (int i = sub >> 3; i < 4 * (k1 - k0); i += kCleaners / 8) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(v_piece(v, k0, i, sub));
+    unsigned dims = 0;                          // of the piece's eight
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const unsigned bad = not_finite(w[e]);
+      if (!bad) continue;
+      if (bad & 0x8000u) w[e] &= 0xffff0000u;
+      if (bad >> 31) w[e] &= 0x0000ffffu;
+      dims |= ((bad >> 15 & 1u) | (bad >> 30 & 2u)) << (2 * e);
+    }
+    if (!dims) continue;
+    const int k = k0 + (i >> 2), s = key0 + k;
+    const int dim = dim0 + 64 * (i & 3) + 8 * ((sub ^ k) & 7);
+#pragma unroll 1
+    for (int r = 0; r < nrows; ++r) {
+      const int pos = pos0 + r / A.H;
+      if (s > min(pos, last) || (A.window && s <= pos - A.window && s >= A.sinks)) continue;
+      // once all warps have come to this tile, none has to read what the piece
+      // before has lost
+      if (!ready && !wait1(o_ok, parity, abort_flag, err)) return;
+      ready = true;
+      atomicOr(&lost[r][dim >> 5], dims << (dim & 31));
+    }
+  }
+}
+// Makes the noted dims (256 from TMEM column o_cols on) of each lane's row NaN, and
+// forgets them.
+__device__ __noinline__ void spoil_lost(unsigned* lost, uint32_t o_cols) {
+#pragma unroll 1
+  for (int cc = 0; cc < 8; ++cc) {
+    const unsigned bits = lost[cc];
+    lost[cc] = 0;
+    float o[32];
+    tmem_ld32(o_cols + 32 * cc, o);
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if ((bits >> e) & 1u) o[e] = __int_as_float(0x7fffffff);
+    tmem_st32(o_cols + 32 * cc, o);
+  }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v,
@@ -395,6 +460,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                            return item_geom(A, i).tiles + kItemCost;
                          });
   }
+  static_assert(sizeof(so.lost) == kThreads * sizeof(uint4), "one store a thread");
+  if (rank == 1) reinterpret_cast<uint4*>(so.lost)[threadIdx.x] = make_uint4(0, 0, 0, 0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -918,8 +985,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           if (lane == 0) mbar_arrive(smem_u32(&so.o_ok[sl4]));
           // Keys that some row does not see have zeros in its P, and a zero
           // times a NaN or infinite value would reach that row: such values
-          // become 0 (a row that sees them has a NaN logit). PV of this unit
-          // waits for `clean`.
+          // become 0, and the rows that see them get theirs at the end. PV of
+          // this unit waits for `clean`.
           for (int u = 0; u < n; ++u, vc += 2) {
             const unsigned long long hidden =
                 2 * t + u < x.nu ? unit_hidden(A, x, 2 * t + u) : 0ull;
@@ -934,22 +1001,17 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int h = 0; h < 2; ++h) {
               const int c = vc + h;
               if (!(ok = wait32(so.v_full[c & 3], (c >> 2) & 1, abort_flag, err))) break;
-              auto clean = [](uint32_t w) {
-                if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-                if ((w & 0x7f800000u) == 0x7f800000u) w &= 0x0000ffffu;
-                return w;
-              };
-              // rows k0 .. k1 - 1 of the chunk's four atoms, 8 x 16 B each
               uint8_t* v = so.v[c & 3];
               const int sub = static_cast<int>(threadIdx.x) - 128;
+              unsigned bad = 0;
 #pragma unroll 2
-              for (int i = sub >> 3; i < 4 * (k1 - k0); i += 32) {
-                uint4* at = reinterpret_cast<uint4*>(v + (i & 3) * kUnitAtom +
-                                                     (k0 + (i >> 2)) * 128 + (sub & 7) * 16);
-                const uint4 o = *at;
-                const uint4 w = make_uint4(clean(o.x), clean(o.y), clean(o.z), clean(o.w));
-                if (w.x != o.x || w.y != o.y || w.z != o.z || w.w != o.w) *at = w;
+              for (int i = sub >> 3; i < 4 * (k1 - k0); i += kCleaners / 8) {
+                const uint4 o = *v_piece(v, k0, i, sub);
+                bad |= not_finite(o.x) | not_finite(o.y) | not_finite(o.z) | not_finite(o.w);
               }
+              if (bad)
+                clean_v(A, v, k0, k1, sub, unit_block(x, 2 * t + u) * 64, 256 * h, x.pos0, x.last,
+                        x.nrows, so.lost, so.o_ok[sl4], (tc >> 2) & 1, abort_flag, err);
             }
             if (!ok) break;
             fence_proxy_async_smem();
@@ -968,6 +1030,11 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         (a1.x > -INFINITY ? a1.y * fast_exp2(a1.x - m) : a1.y);
         if (!(ok = wait32(ctl.o_done, pieces & 1, abort_flag, err))) break;
         tc_fence_after();
+        const uint4 lost0 = *reinterpret_cast<const uint4*>(&so.lost[r][8 * g]);
+        const uint4 lost1 = *reinterpret_cast<const uint4*>(&so.lost[r][8 * g + 4]);
+        if (__any_sync(0xffffffffu, (lost0.x | lost0.y | lost0.z | lost0.w | lost1.x | lost1.y |
+                                     lost1.z | lost1.w) != 0u))
+          spoil_lost(&so.lost[r][8 * g], o_cols);
         const bool valid = r < x.nrows;
         if (p.first && p.last) {
           const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -198,3 +198,71 @@ def test_a_split_call_is_joined_whatever_the_error_word_says(dsa):  # noqa: F811
     no_device_error(dsa)
     assert (out == 7).all() and (lse == 7).all()
     halves.close()
+
+
+# ------------------------------------------- infinite values that rows do see
+
+def check_infinite_rows(out, lse, q, k, see):
+    """Rows over keys of which some are infinite in single dims. A logit of +inf or NaN
+    makes the row NaN; one of -inf has no weight, and 0 times the key's infinite value
+    makes that dim of the row NaN, and no other."""
+    with np.errstate(invalid="ignore"):
+        z = q.double().cpu().numpy() @ k.T
+    whole = (see & ~(z < np.inf)).any(1)
+    part = ~whole
+    assert torch.isnan(out[torch.from_numpy(whole).to(out.device)].float()).all()
+    assert not torch.isfinite(lse[torch.from_numpy(whole).to(out.device)]).any()
+    inf = np.isinf(k)
+    dims = (see.astype(np.float32) @ inf[:, :512].astype(np.float32) > 0)[part]
+    rows = torch.from_numpy(np.nonzero(part)[0]).to(out.device)
+    got = out[rows].clone()
+    want = torch.from_numpy(dims).to(out.device)
+    assert torch.equal(torch.isnan(got.float()), want)
+    finite = see[part] & np.isfinite(z[part])
+    k0 = np.where(inf, 0.0, k)
+    from test_cache_attention import plain
+    ref = plain(q[rows].double().cpu().numpy(), k0, finite)[0]
+    got[want] = torch.from_numpy(ref).to(out.device)[want].to(got.dtype)
+    check_rows(got, lse[rows], q[rows], k0, finite)
+    return int(whole.sum()), int(dims.any(1).sum())
+
+
+@pytest.mark.parametrize("H,sinks,window", [(8, 0, 40), (128, 3, 40), (65, 70, 200), (1, 2, 1000)])
+def test_window_prefill_over_single_infinite_values(dsa, H, sinks, window):  # noqa: F811
+    """Keys seen by all rows of a tile, by some, and by none, in rows of whole units and
+    of cut ones; in dims of both halves, the rope dims, several dims and several keys."""
+    g = torch.Generator(device="cuda").manual_seed(70 + H)
+    T = 190
+    q, kv = randn(g, T, H, 576), randn(g, T, 576)
+    # queries on one side of the infinities, so that a third of them meets -inf alone
+    spots = [(0, 5, 1), (2, 300, -1), (63, 511, 1), (64, 0, 1), (64, 256, 1), (100, 255, -1),
+             (101, 570, 1), (130, 17, 1), (131, 17, -1), (189, 448, 1)]
+    for s, d, sign in spots:
+        kv[s, d] = sign * float("inf")
+        side = (torch.arange(T, device="cuda") % 3 == 0).view(T, 1)
+        q[:, :, d] = torch.where(side, q[:, :, d], q[:, :, d].abs() * -sign)
+    q[:, :, 17] = randn(g, T, H)
+    out, lse = dsa.window_mla(q, kv, sinks, window, SM)
+    no_device_error(dsa)
+    k = kv.double().cpu().numpy()
+    see = np.stack([sees(t, T, sinks, window) for t in range(T)]).repeat(H, 0)
+    whole, some = check_infinite_rows(out.view(-1, 512), lse.view(-1), q.view(-1, 576), k, see)
+    assert whole > T * H // 8 and some > T * H // 8
+
+
+@pytest.mark.parametrize("nq,H,lens", [(3, 8, [700, 65]), (2, 128, [9000, 130]), (4, 32, [20001])])
+def test_split_decode_over_single_infinite_values(dsa, nq, H, lens):  # noqa: F811
+    """The same in a paged cache, in sequences whose parts are joined."""
+    c = packed_cache(lens, 80 + nq)
+    q = randn(c["g"], len(lens), nq, H, 576)
+    for b, n in enumerate(lens):
+        for s, d in ((n - 1, 3), (n - 2, 400), (n - nq, 77), (n // 2, 130), (5, 511)):
+            c["kv_pool"][int(c["block_table"][b, s // 64]), s % 64, d] = float("inf")
+            q[b, :, ::2, d] = -q[b, :, ::2, d].abs()
+    out, lse = dsa.split_mla_decode_paged(q, c["kv_pool"], c["block_table"], c["seq_len"], SM)
+    no_device_error(dsa)
+    for b, n in enumerate(lens):
+        see = np.stack([sees(n - nq + j, n, 0, 0) for j in range(nq)]).repeat(H, 0)
+        whole, some = check_infinite_rows(out[b].view(-1, 512), lse[b].view(-1),
+                                          q[b].view(-1, 576), seq_rows(c, b), see)
+        assert whole > 0 and some >= nq * H // 2
