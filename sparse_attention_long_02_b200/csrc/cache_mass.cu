@@ -49,7 +49,7 @@ struct MassSmem {
   unsigned long long s_full[2], s_empty[2];
   unsigned long long done;                      // completes only in the give-up path
   uint32_t tmem_base;
-  int abort_flag;
+  int abort_flag[2];                            // (no wait is for more than a tile: [1] stays 0)
 };
 static_assert(sizeof(MassSmem) + 1024 <= 232448, "fits the 227 KB of shared memory a CTA may use");
 
@@ -108,7 +108,8 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       init(sm.s_full[i], 1);
       init(sm.s_empty[i], 4);
     }
-    sm.abort_flag = launch_aborted(err) ? 1 : 0;
+    sm.abort_flag[0] = launch_aborted(err) ? 1 : 0;
+    sm.abort_flag[1] = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -119,7 +120,7 @@ mass_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem_base;
-  volatile int* abort_flag = &sm.abort_flag;
+  volatile int* abort_flag = sm.abort_flag;
   MassWalk walk(sm.share);
   bool ok = *abort_flag == 0;
 

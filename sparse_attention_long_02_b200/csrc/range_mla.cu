@@ -295,7 +295,7 @@ struct Ctl {
   Share share;                                  // of the row tiles' weights
   unsigned long long piece_full[kPieces];
   uint32_t tmem_base;
-  int abort_flag;
+  int abort_flag[2];                            // and the CTA's progress: tiles of QK, of PV
 };
 constexpr size_t kSmemBytes = kBig + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "fits the 227 KB of shared memory a CTA may use");
@@ -434,7 +434,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       init(ctl.ml_free, 8);
       init(ctl.o_done, 1);
       if (rank == 1) init(so.ml_full, 8);
-      ctl.abort_flag = launch_aborted(err) ? 1 : 0;
+      ctl.abort_flag[0] = launch_aborted(err) ? 1 : 0;
+      ctl.abort_flag[1] = 0;
     }
     fence_barrier_init();
   } else if (warp == 1) {
@@ -478,7 +479,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   }
   cluster_wait();
   const uint32_t tmem = ctl.tmem_base;
-  volatile int* abort_flag = &ctl.abort_flag;
+  volatile int* abort_flag = ctl.abort_flag;
   bool ok = *abort_flag == 0;
   // The later pieces are written down by CTA 1's warp 13 for every role of both
   // CTAs (the arithmetic is cold code that each role would wait for between two
@@ -659,6 +660,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int kk = 0; kk < 4; ++kk) mma_bf16(d, rope_d + 2 * kk, kr_d + 2 * kk, id, 1u);
             mma_commit(smem_u32(&ctl.kr_empty));
             mma_commit(smem_u32(&ctl.s_full[sb]));
+            abort_flag[1] = tc;
             if (t + 1 == p.t1) mma_commit(smem_u32(&ctl.q_free));
           }
         }
@@ -892,6 +894,7 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               mma_commit(smem_u32(&so.p_free[slot]));
             }
             mma_commit(smem_u32(&so.pv_done[tc & 3]));
+            abort_flag[1] = tc;
           }
           mma_commit(smem_u32(&ctl.o_done));
         }

@@ -12,9 +12,15 @@ namespace dsa {
 //
 // The slow path suspends the warp in the barrier unit, at most a millisecond at
 // a time, and spends no issue slots that the SM's other warps could use.
+//
+// A wait may be for the whole of a row tile that another role works on, which for
+// a very long cache takes over a second: the limit counts from the CTA's last
+// progress, a number that one of its roles changes with each tile (abort_flag[1];
+// a tile takes microseconds).
 static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity,
                                               volatile int* abort_flag, unsigned* err) {
-  const unsigned long long t0 = globaltimer();
+  unsigned long long t0 = globaltimer();
+  int tiles = abort_flag[1];
   while (true) {
     uint32_t ok;
     asm volatile(
@@ -27,6 +33,12 @@ static __device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity,
     if (ok) return true;
     if (*abort_flag) return false;
     if (globaltimer() - t0 > kWaitLimitNs) {
+      const int now = abort_flag[1];
+      if (now != tiles) {
+        tiles = now;
+        t0 = globaltimer();
+        continue;
+      }
       *abort_flag = 1;
       raise_error(err, kErrTimeout);
       return false;

@@ -266,3 +266,23 @@ def test_split_decode_over_single_infinite_values(dsa, nq, H, lens):  # noqa: F8
         whole, some = check_infinite_rows(out[b].view(-1, 512), lse[b].view(-1),
                                           q[b].view(-1, 576), seq_rows(c, b), see)
         assert whole > 0 and some >= nq * H // 2
+
+
+def test_row_tiles_that_take_over_a_second(dsa):  # noqa: F811
+    """75 sequences of a hundred million tokens that share four blocks, so that roles
+    wait for the end of a row tile longer than the limit of a wait that makes no
+    progress. Queries of 0 see all keys alike: a weight's sum is exact (multiples of 64
+    below 2^30). A value's sum is one of n / 16 steps of the tensor core, which holds it
+    in fp32 and may cut where it does not round: off by 2^-23 a step, 0.75 in all."""
+    blocks = 100_000_000 // 64 // 4 * 4
+    B, n = 75, blocks * 64
+    v = 2.0 ** (torch.arange(576, device="cuda") % 3)
+    kv = v.to(torch.bfloat16).expand(4, 64, 576).contiguous()
+    table = torch.arange(4, dtype=torch.int32, device="cuda").repeat(B, blocks // 4)
+    q = torch.zeros(B, 1, 1, 576, dtype=torch.bfloat16, device="cuda")
+    lens = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    no_device_error(dsa)
+    out, lse = dsa.split_mla_decode_paged(q, kv, table, lens, SM)
+    no_device_error(dsa)
+    assert ((out.float() - v[:512]).abs() <= n / 16 * 2.0 ** -23 * v[:512]).all()
+    assert (lse.double() - np.log(n)).abs().max() <= 8 * 2.0 ** -24 * np.log(n)
