@@ -53,6 +53,29 @@ def test_decode_of_thousands_of_short_sequences(dsa, B, nq, H, most, window):  #
         check_rows(out[b].view(-1, 512), lse[b].view(-1), q[b].view(-1, 576), seq_rows(c, b), see)
 
 
+@pytest.mark.parametrize("T,H,sinks,window,ragged", [
+    (2500, 128, 4, 70, 0),        # equal shares or whole row tiles: 34 of them a cluster
+    (2501, 65, 0, 130, 300),      # the same, the first rows with less and less to see
+    (16500, 65, 3, 40, 0),        # too many row tiles to scan: whole ones, no workspace
+    (16385, 128, 0, 9, 0)])
+def test_window_prefill_of_thousands_of_row_tiles(dsa, T, H, sinks, window, ragged):  # noqa: F811
+    g = torch.Generator(device="cuda").manual_seed(T + H)
+    S = T - ragged                                      # rows past the cache see less
+    q, kv = randn(g, T, H, 576), randn(g, S, 576)
+    assert (dsa.window_mla_workspace_size(T, S, H, 0, sinks, window) == 0) == (T > 16384)
+    out, lse = dsa.window_mla(q, kv, sinks, window, SM)
+    no_device_error(dsa)
+    k = kv.double().cpu().numpy()
+    # 16 rows of every 90 and the last: pieces of all places and turns of the shares' rings
+    for t0 in [*range(0, T - 16, 90), T - 16]:
+        lo = max(0, min(S, t0 - window + 1))
+        hi = min(S, t0 + 16)
+        cols = np.unique(np.concatenate([np.arange(min(sinks, S)), np.arange(lo, hi)]))
+        see = np.stack([sees(t, S, sinks, window)[cols] for t in range(t0, t0 + 16)]).repeat(H, 0)
+        check_rows(out[t0:t0 + 16].reshape(-1, 512), lse[t0:t0 + 16].reshape(-1),
+                   q[t0:t0 + 16].reshape(-1, 576), k[cols], see)
+
+
 # ------------------------------------- a call cut between its two launches
 
 class Halves:
