@@ -1305,10 +1305,9 @@ size_t range_layout(RangeArgs& a, void* workspace) {
                                 (std::min<long long>(a.sinks, keys) + 63) / 64);
   const long long tiles = (units + 1) / 2;
   a.whole = !a.block_table && items > kScanItems;
-  a.clusters = static_cast<int>(std::min<long long>(
-      kMaxClusters, std::max(1ll, items * (tiles + kItemCost))));
+  a.clusters = static_cast<int>(std::min<long long>(kMaxClusters, items * (tiles + kItemCost)));
   a.rows_pad = (a.G * a.H + 7) / 8 * 8;
-  if (a.whole || a.clusters == 1) {
+  if (a.whole) {
     a.rec = nullptr;
     a.part_ml = nullptr;
     a.part_o = nullptr;
