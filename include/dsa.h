@@ -490,7 +490,8 @@ int dsa_split_mla_decode_paged(const void *q, const void *kv_pool, const int32_t
  *   past the cache may see no key (out 0, lse -inf). q_pos0 + T and S at most
  *   2^30. window >= q_pos0 + T is dense causal attention.
  *   workspace: dsa_window_mla_workspace_size(T, S, H, q_pos0, sinks, window)
- *   bytes (few rows are split over the keys, as in a decode; 0 for many).
+ *   bytes (few rows are split over the keys, as in a decode; for many, 0
+ *   unless a row may see more than some 131000 keys).
  * dsa_window_mla_decode_paged: the same mask for the nq new tokens of each
  *   sequence of a paged cache; arguments, workspace and faults as for
  *   dsa_split_mla_decode_paged. Blocks no query sees may have any table entry.

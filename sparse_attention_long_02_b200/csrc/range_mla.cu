@@ -91,6 +91,12 @@ constexpr int kItemCost = 3;                    // a row tile's fixed cost, in t
 // 1024: 2.77 ms whole, 2.84 ms cut; 64 x 32768 tokens: 683 us whole, 656 us cut;
 // one sequence of 131072: 2393 us whole, 67 us cut.)
 constexpr int kCutCostFew = 5, kCutCostMany = 7;
+// Tiles whose sums the tensor core adds up before they move to a second sum in
+// memory. Its fp32 additions cut where they do not round, so a sum of n keys of
+// like weights comes out too small by up to n / 16 2^-23: measured 0.02% at 32768
+// keys, 0.08% at 131072, 0.6% at a million (more than the output's rounding), 10%
+// at 16 million.
+constexpr int kSumTiles = 1024;
 
 struct LogitsSmem {                             // CTA 0
   uint8_t ring[kRing][kEntry];                  // K's latent dims, and Q on its way to TMEM
@@ -363,6 +369,33 @@ __device__ __noinline__ void clean_v(const RangeArgs& A, uint8_t* v, int k0, int
       ready = true;
       atomicOr(&lost[r][dim >> 5], dims << (dim & 31));
     }
+  }
+}
+// Adds the 256 dims of O (of each lane's row) to the sum in memory, scaled for the
+// reference maximum of now (`fresh`: there is none yet), and starts O anew; at a
+// piece's `end` adds that sum to O instead. Each thread meets its own floats only.
+__device__ __noinline__ void move_sum(float4* sum, int pitch, bool valid, float scale, bool fresh,
+                                      bool end, uint32_t o_cols) {
+#pragma unroll 1
+  for (int cc = 0; cc < 8; ++cc) {
+    float o[32];
+    tmem_ld32(o_cols + 32 * cc, o);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float4* at = sum + static_cast<long long>(8 * cc + e) * pitch;
+      float4 a = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      if (valid && !fresh) {
+        const float4 old = *at;
+        a = make_float4(fmaf(old.x, scale, a.x), fmaf(old.y, scale, a.y), fmaf(old.z, scale, a.z),
+                        fmaf(old.w, scale, a.w));
+      }
+      if (valid && !end) *at = a;
+      o[4 * e] = end ? a.x : 0.f;
+      o[4 * e + 1] = end ? a.y : 0.f;
+      o[4 * e + 2] = end ? a.z : 0.f;
+      o[4 * e + 3] = end ? a.w : 0.f;
+    }
+    tmem_st32(o_cols + 32 * cc, o);
   }
 }
 // Makes the noted dims (256 from TMEM column o_cols on) of each lane's row NaN, and
@@ -962,6 +995,12 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const uint32_t o_cols = tmem + (static_cast<uint32_t>(32 * wq) << 16) + 256 * g;
       int tc = 0, vc = 0;
       bool recorded = false;
+      // a long piece's second sum: the place of its part, or of the next one
+      float scale = 1.f;
+      auto sum = [&]() {
+        return A.part_o + (2ll * cluster + (p.first ? 1 : 0)) * 128 * A.rows_pad +
+               64ll * g * A.rows_pad + r;
+      };
       for (; next_piece(true); ++pieces) {
         for (int t = p.t0; ok && t < p.t1; ++t, ++tc) {
           const int n = tile_units(x, t);
@@ -969,7 +1008,10 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           if (!(ok = wait32<true>(so.al_full[sl4], (tc >> 2) & 1, abort_flag, err))) break;
           if (threadIdx.x == 128) mbar_expect_tx(smem_u32(&so.al_full[sl4]), 512);
           const float alpha = so.alpha[sl4][r];
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+          const int age = t - p.t0;
+          const bool full = age > 0 && age % kSumTiles == 0;
+          if (age > kSumTiles) scale *= alpha;
+          if (__any_sync(0xffffffffu, alpha != 1.f) || full) {
             // never on a piece's first tile, so the PV of the tile before is this piece's
             if (!(ok = wait32(so.pv_done[(tc + 3) & 3], ((tc - 1) >> 2) & 1, abort_flag, err)))
               break;
@@ -981,6 +1023,10 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] *= alpha;
               tmem_st32(o_cols + 32 * cc, o);
+            }
+            if (full) {
+              move_sum(sum(), A.rows_pad, r < x.nrows, scale, age == kSumTiles, false, o_cols);
+              scale = 1.f;
             }
           }
           tc_fence_before();
@@ -1033,6 +1079,8 @@ range_mla_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         (a1.x > -INFINITY ? a1.y * fast_exp2(a1.x - m) : a1.y);
         if (!(ok = wait32(ctl.o_done, pieces & 1, abort_flag, err))) break;
         tc_fence_after();
+        if (p.t1 - p.t0 > kSumTiles)
+          move_sum(sum(), A.rows_pad, r < x.nrows, scale, false, true, o_cols);
         const uint4 lost0 = *reinterpret_cast<const uint4*>(&so.lost[r][8 * g]);
         const uint4 lost1 = *reinterpret_cast<const uint4*>(&so.lost[r][8 * g + 4]);
         if (__any_sync(0xffffffffu, (lost0.x | lost0.y | lost0.z | lost0.w | lost1.x | lost1.y |
@@ -1307,20 +1355,23 @@ size_t range_layout(RangeArgs& a, void* workspace) {
   a.whole = !a.block_table && items > kScanItems;
   a.clusters = static_cast<int>(std::min<long long>(kMaxClusters, items * (tiles + kItemCost)));
   a.rows_pad = (a.G * a.H + 7) / 8 * 8;
-  if (a.whole) {
-    a.rec = nullptr;
-    a.part_ml = nullptr;
-    a.part_o = nullptr;
-    return 0;
-  }
+  a.rec = nullptr;
+  a.part_ml = nullptr;
+  a.part_o = nullptr;
+  if (a.whole && tiles <= kSumTiles) return 0;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   const size_t n = static_cast<size_t>(a.clusters);
   const size_t rec = up(n * sizeof(int2)), ml = up(2 * n * a.rows_pad * sizeof(float2));
+  const size_t parts = 2 * n * 128 * a.rows_pad * sizeof(float4);
   char* ws = static_cast<char*>(workspace);
+  if (a.whole) {                                // no row tile is cut: second sums only
+    a.part_o = reinterpret_cast<float4*>(ws);
+    return parts;
+  }
   a.rec = reinterpret_cast<int2*>(ws);
   a.part_ml = ws ? reinterpret_cast<float2*>(ws + rec) : nullptr;
   a.part_o = ws ? reinterpret_cast<float4*>(ws + rec + ml) : nullptr;
-  return rec + ml + 2 * n * 128 * a.rows_pad * sizeof(float4);
+  return rec + ml + parts;
 }
 
 cudaError_t launch_range_mla(const RangeArgs& a_in, cudaStream_t st) {

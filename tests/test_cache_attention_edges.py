@@ -309,3 +309,70 @@ def test_row_tiles_that_take_over_a_second(dsa):  # noqa: F811
     no_device_error(dsa)
     assert ((out.float() - v[:512]).abs() <= n / 16 * 2.0 ** -23 * v[:512]).all()
     assert (lse.double() - np.log(n)).abs().max() <= 8 * 2.0 ** -24 * np.log(n)
+
+
+# ------------------------------------------------- sums over millions of keys
+
+def check_long_rows(out, lse, q, k, times):
+    """Rows over keys k [n, 576] that each occur `times` often, in 64 bits on the GPU.
+
+    A value's sum is added up by the tensor core in runs of 131072 keys, 16 keys a step
+    that may cut where it does not round: 8192 2^-23 = 2^-10 of sum p |v|. The runs and
+    the weights are added up in fp32, a term for 128 keys. The rest as in check_rows."""
+    n = float(times.sum())
+    q, k = q.double(), k.double()
+    z = SM * (q @ k.T) + times.double().log()
+    ref_lse = torch.logsumexp(z, 1, keepdim=True)
+    p = (z - ref_lse).exp()
+    ref, absum = p @ k[:, :512], p @ k[:, :512].abs()
+    dz = SM * 580 * 2.0 ** -24 * q.norm(dim=1, keepdim=True) * k.norm(dim=1).max()
+    run = (n / 128 + 128) * 2.0 ** -24
+    tol_lse = 2 * dz + 2 * run + 2.0 ** -20 * (1 + ref_lse.abs())
+    off = (lse.double().view(-1, 1) - ref_lse).abs()
+    assert (off <= tol_lse).all(), (off.max(), tol_lse.min())
+    tol = (2.0 ** -8 + 2 * tol_lse + 2.0 ** -18 + 2.0 ** -10 + run) * absum + 2.0 ** -8 * ref.abs()
+    bad = (out.double() - ref).abs() > tol
+    assert not bad.any(), ((out.double() - ref).abs()[bad][:4], tol[bad][:4])
+
+
+@pytest.mark.parametrize("B,late", [(75, 0), (75, 2048), (3, 64), (148, 0)])
+def test_split_decode_of_millions_of_tokens(dsa, B, late):  # noqa: F811
+    """Four million tokens a sequence out of few blocks, values all positive: row tiles in
+    one share and cut ones. The last `late` blocks draw e^6.25 times the weight, so that
+    the reference maximum of what was summed before them moves."""
+    g = torch.Generator(device="cuda").manual_seed(B + late)
+    blocks, H = 65536, 2
+    kv = torch.rand(32, 64, 576, generator=g, device="cuda").to(torch.bfloat16)
+    kv[16:, :, :512] += 2
+    kv[:, :, 575] = 0
+    kv[16:, :, 575] = 6.25
+    q = randn(g, B, 1, H, 576)
+    q[..., :512] *= 0.1                                 # the values' size says little
+    q[..., 575] = 24
+    early = torch.arange(blocks - late, dtype=torch.int32, device="cuda") % 16
+    row = torch.cat([early, 16 + torch.arange(late, dtype=torch.int32, device="cuda") % 16])
+    lens = torch.full((B,), blocks * 64, dtype=torch.int32, device="cuda")
+    out, lse = dsa.split_mla_decode_paged(q, kv, row.repeat(B, 1), lens, SM)
+    no_device_error(dsa)
+    times = torch.bincount(row, minlength=32).repeat_interleave(64)
+    k = kv.view(-1, 576)[times > 0]
+    check_long_rows(out.view(-1, 512), lse.view(-1), q.view(-1, 576), k, times[times > 0])
+
+
+def test_window_prefill_of_whole_row_tiles_over_long_prefixes(dsa):  # noqa: F811
+    """Too many row tiles to scan, each longer than a run of the tensor core's sums: the
+    call needs a workspace, which ends where it says."""
+    g = torch.Generator(device="cuda").manual_seed(99)
+    T, H, p0 = 16385, 65, 150000
+    S = p0 + T
+    kv = torch.rand(S, 576, generator=g, device="cuda").to(torch.bfloat16)
+    q = randn(g, T, H, 576)
+    need = dsa.window_mla_workspace_size(T, S, H, p0, 0, S)
+    assert need > 0 and dsa.window_mla_workspace_size(T, S, H, p0, 4, 130000) == 0
+    ws = torch.full((need + 4096,), 171, dtype=torch.uint8, device="cuda")
+    out, lse = dsa.window_mla(q, kv, 0, S, SM, q_pos0=p0, workspace=ws[:need])
+    no_device_error(dsa)
+    assert (ws[need:] == 171).all()
+    for t in (0, 73, 74, 9000, T - 1):
+        k = kv[:p0 + t + 1]
+        check_long_rows(out[t], lse[t], q[t], k, torch.ones(len(k), device="cuda"))
