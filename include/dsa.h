@@ -82,6 +82,9 @@ const char *dsa_last_error_string(void);
  * Synchronises `stream`, then reads and clears the current device's error
  * word. Returns DSA_OK, DSA_ERR_TIMEOUT (takes precedence) or
  * DSA_ERR_DEVICE_BOUNDS; DSA_ERR_CUDA if the synchronisation itself failed.
+ * The word is the device's, not the stream's: while a timeout is pending,
+ * calls on every stream return at once, so results of those that were in
+ * flight on any stream when it was recorded may be incomplete.
  */
 int dsa_get_device_error(dsa_stream_t stream);
 
@@ -89,11 +92,12 @@ int dsa_get_device_error(dsa_stream_t stream);
  * Debug aid for failure handling; the pages have no counterpart. With a bit
  * of `mask` set, every later launch of the named kernel on the current
  * device first makes its MMA-issuing thread wait on a barrier that nothing
- * arrives at. That wait, bounded like every wait in the library (1 s), runs
- * out; the kernel records DSA_ERR_TIMEOUT in the device's error word and
- * leaves through its give-up path (every CTA drains its own copies in
- * flight and frees its tensor memory), and later kernels of the library
- * return at once until dsa_get_device_error() clears the word. Nothing
+ * arrives at. That wait, bounded like every wait in the library (1 s, or 1 s
+ * without progress of its CTA), runs out; the kernel records DSA_ERR_TIMEOUT
+ * in the device's error word and leaves through its give-up path (every CTA
+ * drains its own copies in flight and frees its tensor memory), and later
+ * calls of the library return at once until dsa_get_device_error() clears the
+ * word. Nothing
  * faults or traps. mask = 0 restores normal operation.
  *   DSA_DEBUG_STALL_INDEXER  the indexer (dsa_indexer_scores, and the
  *                            indexer launches inside dsa_forward,
@@ -521,7 +525,8 @@ int dsa_window_mla_decode_paged(const void *q, const void *kv_pool, const int32_
  *             needs no clearing; entries from seq_len[b] on are not written
  *
  *   lse     [B][nq][H] fp32 as dsa_split_mla_decode_paged returns it for the
- *           same queries; a query whose lse is -inf gives nothing
+ *           same queries; a query whose lse is -inf gives nothing. The weights
+ *           are those of dense attention: there is no windowed form.
  *   mass    [B][ld] fp32, indexed by the token's slot, ld >= 64 * max_blocks
  *   other arguments and faults as for dsa_split_mla_decode_paged; the keys of
  *   a bad block id keep their totals. Every total is summed by one thread in
@@ -534,8 +539,8 @@ int dsa_attention_mass_paged(const void *q, const void *kv_pool, const int32_t *
 
 /*
  * Eviction from the paged caches by accumulated attention weight, in place.
- * The pages keep every token; this is the companion of the dense and windowed
- * decode above for contexts that outgrow the cache.
+ * The pages keep every token; this is the companion of the dense decode above
+ * for contexts that outgrow the cache.
  *
  * A sequence of at most `budget` tokens is left as it is. A longer one keeps
  * its first `sinks` tokens, its last `recent` tokens and, of those between,

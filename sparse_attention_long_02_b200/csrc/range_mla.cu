@@ -6,7 +6,9 @@
 // with s <= min(p, last key) and, with a window w, s > p - w or s < sinks:
 //   out = sum_s exp(z_s - lse) kv[s, :512],  z_s = sm_scale q . kv[s],
 //   lse = log sum_s exp(z_s).
-// A row that sees no key gets out = 0 and lse = -inf.
+// A row that sees no key gets out = 0 and lse = -inf. What a row does not see has
+// no effect on it; an infinite value that it does see with no weight (logit -inf)
+// makes that dim NaN, any other infinity or NaN the whole row.
 //
 // Row tiles. The MMA's M holds 128 rows: all heads of G = min(queries, 128 / H)
 // consecutive queries of one sequence, which share the keys they read. A row
@@ -17,8 +19,8 @@
 // TMEM columns of an SM, so one SM cannot hold it beside the logits. CTA 0
 // forms the logits and the softmax, CTA 1 the output:
 //   CTA 0: Q's 512 latent dims move into TMEM (256 columns; the rope dims stay
-//     in shared memory), K chunks (128 keys x 64 dims) stream through a ring of
-//     TMA loads; S = Q K^T (M = 128, N = 128, K = 576) goes into one of two
+//     in shared memory), K's latent dims stream through a ring of TMA loads (128
+//     keys x 128 dims an entry), its rope dims through a place of their own; S = Q K^T (M = 128, N = 128, K = 576) goes into one of two
 //     TMEM buffers; two groups of four warps (thread = row) take 64 keys of a
 //     tile each: row maximum, running reference maximum (re-based only when it
 //     grows by more than 8 in log2 units), P = exp2(z - m) in bf16 into shared
@@ -26,9 +28,11 @@
 //   CTA 1: V chunks (64 keys x 256 dims) stream through their own ring;
 //     O (+)= P V (M = 128, N = 256 twice, K = 64); eight warps rescale O in
 //     TMEM when a reference maximum moved, and write the result.
-// Nothing below fp32 crosses but P, which the PV product takes in bf16. Each
-// role streams its own operand, K from HBM and V, the same rows two tiles later,
-// from L2. (Asking L2 for tiles ahead of the loads does not pay: its lines are
+// Nothing below fp32 crosses but P, which the PV product takes in bf16: half a step
+// (2^-8) of each weight at most, which for many keys averages out below the
+// output's own rounding (error of the outputs against 64 bits 1.7e-3 to 1.8e-3,
+// 1.5e-3 to 1.7e-3 with P in fp32). l sums P before that rounding. Each role streams
+// its own operand, K from HBM and V, the same rows two tiles later, from L2. (Asking L2 for tiles ahead of the loads does not pay: its lines are
 // lost again before they are used; 64 x 32768 tokens read 797 MB for 456 when it
 // ran six tiles ahead.)
 //
@@ -45,11 +49,12 @@
 // dims of Q, P in and out), 2900 cycles at 128 B each. Measured, a tile takes 3400
 // cycles with the cache in L2 (64 sequences of 32768 tokens that share 37 MB: 472
 // us), where the softmax's 2700 and its waits set the pace and QK waits 450 for a
-// buffer, and 3850 from HBM (595 us, 4.1 TB/s), where QK waits 1000 for K. That run
-// is held at 1.5 GHz of 1.97 by the board's 1000 W; short calls run at full clock,
-// and their time is the way to the first tile (9 us), the shares' tiles (2 to 2.3
-// us each), a part's way to memory (5 us: an SM writes some 30 B a cycle) and the
-// join (7 us): one sequence of 131072 tokens 62 us.
+// buffer, and 3850 from HBM (20 calls in a row 595 us, 4.1 TB/s), where QK waits
+// 1000 for K. Those are held at 1.5 GHz of 1.97 by the board's 1000 W, and a loop of
+// calls that lasts seconds at 1.37 GHz (692 us, 3.5 TB/s). Short calls run at full
+// clock, and their time is the way to the first tile (9 us), the shares' tiles (2 to
+// 2.3 us each), a part's way to memory (5 us: an SM writes some 30 B a cycle) and
+// the join (7 us): one sequence of 131072 tokens 62 us.
 //
 // CTA 0's shared memory is full to the last bytes. The rope dims of K in a place of
 // their own, not in the ring, took 64 x 32768 from 635 to 595 us; what paid for
@@ -82,14 +87,14 @@ constexpr int kPieces = 8;                      // pieces written down at a time
 constexpr int kPSlots = 4;
 constexpr int kVRing = 4;
 constexpr float kRebase = 8.0f;                 // lazy rescale threshold (log2 units)
-constexpr int kMaxClusters = 74;                // two CTAs on each of 148 SMs
+constexpr int kMaxClusters = 74;                // of two CTAs, one on each of 148 SMs
 constexpr int kScanItems = 16384;               // row tiles a cluster scans for its share
 constexpr int kItemCost = 3;                    // a row tile's fixed cost, in tiles
 // What cutting row tiles costs, in tiles: where there are fewer of them than
 // clusters a cluster writes one part, else two. (Two queries of 64 sequences in a
-// window of 2048: 106 us whole, 118 us cut; a prompt of 8191 rows and a window of
-// 1024: 2.77 ms whole, 2.84 ms cut; 64 x 32768 tokens: 683 us whole, 656 us cut;
-// one sequence of 131072: 2393 us whole, 67 us cut.)
+// window of 2048: 94 to 116 us whole, 117 to 131 us cut; a prompt of 8191 rows and a
+// window of 1024: 2.74 ms whole, 2.76 ms cut; 64 x 32768 tokens: 638 us whole, 626 us
+// cut; one sequence of 131072: 2004 us whole, 61 us cut. In turn on one board.)
 constexpr int kCutCostFew = 5, kCutCostMany = 7;
 // Tiles whose sums the tensor core adds up before they move to a second sum in
 // memory. Its fp32 additions cut where they do not round, so a sum of n keys of

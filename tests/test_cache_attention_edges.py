@@ -376,3 +376,11 @@ def test_window_prefill_of_whole_row_tiles_over_long_prefixes(dsa):  # noqa: F81
     for t in (0, 73, 74, 9000, T - 1):
         k = kv[:p0 + t + 1]
         check_long_rows(out[t], lse[t], q[t], k, torch.ones(len(k), device="cuda"))
+
+
+@pytest.mark.parametrize("lens,budget", [([400_000], 100_003), ([41_500] + [100] * 80, 20_001)])
+def test_evict_of_more_totals_than_shared_memory_holds(dsa, lens, budget):  # noqa: F811
+    """Totals that the selection reads from memory on each pass: past eight CTAs' places,
+    and past one CTA's where the batch leaves a sequence no more."""
+    from test_cache_attention import check_evict, odd
+    check_evict(dsa, lens, budget, 4, 1000, odd, seed=len(lens), alias=True)
