@@ -20,21 +20,24 @@
 // forms the logits and the softmax, CTA 1 the output:
 //   CTA 0: Q's 512 latent dims move into TMEM (256 columns; the rope dims stay
 //     in shared memory), K's latent dims stream through a ring of TMA loads (128
-//     keys x 128 dims an entry), its rope dims through a place of their own; S = Q K^T (M = 128, N = 128, K = 576) goes into one of two
-//     TMEM buffers; two groups of four warps (thread = row) take 64 keys of a
-//     tile each: row maximum, running reference maximum (re-based only when it
-//     grows by more than 8 in log2 units), P = exp2(z - m) in bf16 into shared
-//     memory, one 16 KB bulk copy per 64 keys into CTA 1.
+//     keys x 128 dims an entry), its rope dims through a place of their own;
+//     S = Q K^T (M = 128, N = 128, K = 576) goes into one of two TMEM buffers; two
+//     groups of four warps (thread = row) take 64 keys of a tile each: row
+//     maximum, running reference maximum (re-based only when it grows by more
+//     than 8 in log2 units), P = exp2(z - m) in bf16 into shared memory, one 16 KB
+//     bulk copy per 64 keys into CTA 1.
 //   CTA 1: V chunks (64 keys x 256 dims) stream through their own ring;
 //     O (+)= P V (M = 128, N = 256 twice, K = 64); eight warps rescale O in
 //     TMEM when a reference maximum moved, and write the result.
 // Nothing below fp32 crosses but P, which the PV product takes in bf16: half a step
 // (2^-8) of each weight at most, which for many keys averages out below the
 // output's own rounding (error of the outputs against 64 bits 1.7e-3 to 1.8e-3,
-// 1.5e-3 to 1.7e-3 with P in fp32). l sums P before that rounding. Each role streams
-// its own operand, K from HBM and V, the same rows two tiles later, from L2. (Asking L2 for tiles ahead of the loads does not pay: its lines are
-// lost again before they are used; 64 x 32768 tokens read 797 MB for 456 when it
-// ran six tiles ahead.)
+// 1.5e-3 to 1.7e-3 with P in fp32). l sums P before that rounding.
+//
+// Each role streams its own operand, K from HBM and V, the same rows two tiles
+// later, from L2. (Asking L2 for tiles ahead of the loads does not pay: its lines
+// are lost again before they are used; 64 x 32768 tokens read 797 MB for 456 when
+// it ran six tiles ahead.)
 //
 // Work split. The tiles of all row tiles form one list; each cluster takes an
 // equal share of it, wherever it begins and ends (or whole row tiles in turn,

@@ -7,7 +7,8 @@ import numpy as np
 import pytest
 import torch
 
-from test_cache_attention import SM, check_rows, dsa, randn, sees  # noqa: F401
+from test_cache_attention import (SM, check_evict, check_rows, dsa, odd, plain, randn,  # noqa: F401
+                                  sees)
 from test_gpu_parity import no_device_error
 
 pytestmark = pytest.mark.gpu
@@ -21,7 +22,8 @@ def packed_cache(lens, seed):
     nblk = int(nb.sum()) + 1
     used = torch.arange(max(1, int(nb.max()))).unsqueeze(0) < nb.unsqueeze(1)
     table = torch.full(used.shape, -1, dtype=torch.int32)
-    table[used] = torch.randperm(nblk, generator=g, device="cuda").cpu().to(torch.int32)[:int(nb.sum())]
+    perm = torch.randperm(nblk, generator=g, device="cuda").cpu().to(torch.int32)
+    table[used] = perm[:int(nb.sum())]
     return dict(kv_pool=randn(g, nblk, 64, 576), block_table=table.cuda(),
                 seq_len=lens.to(torch.int32).cuda(), g=g)
 
@@ -243,7 +245,6 @@ def check_infinite_rows(out, lse, q, k, see):
     assert torch.equal(torch.isnan(got.float()), want)
     finite = see[part] & np.isfinite(z[part])
     k0 = np.where(inf, 0.0, k)
-    from test_cache_attention import plain
     ref = plain(q[rows].double().cpu().numpy(), k0, finite)[0]
     got[want] = torch.from_numpy(ref).to(out.device)[want].to(got.dtype)
     check_rows(got, lse[rows], q[rows], k0, finite)
@@ -382,5 +383,4 @@ def test_window_prefill_of_whole_row_tiles_over_long_prefixes(dsa):  # noqa: F81
 def test_evict_of_more_totals_than_shared_memory_holds(dsa, lens, budget):  # noqa: F811
     """Totals that the selection reads from memory on each pass: past eight CTAs' places,
     and past one CTA's where the batch leaves a sequence no more."""
-    from test_cache_attention import check_evict, odd
     check_evict(dsa, lens, budget, 4, 1000, odd, seed=len(lens), alias=True)
